@@ -447,6 +447,125 @@ GEMM_API int gemm_f32_splitk_noalloc(int64_t M, int64_t N, int64_t K, float alph
                                      int64_t ldb, float beta, float *C, int64_t ldc,
                                      int split_k, cudaStream_t stream);
 
+/* ---- the gated feed-forward layer ---------------------------------------
+ *
+ * The operators of one layer of a language model around the GEMM: the gated
+ * block  H = act(X Wg) * (X Wu)  and its gradients, products with 4-bit
+ * weights for a few tokens, and the clipping of all gradients by their
+ * global norm.  All pointers are device pointers unless a line says
+ * otherwise; a call only enqueues work on `stream` and returns, as above.
+ */
+#define GEMM_DT_F32 0   /* float */
+#define GEMM_DT_BF16 1  /* bfloat16 (16 bits, the upper half of a float) */
+
+/* act(g):  SILU       g / (1 + exp(-g))
+ *          GELU       g * (1 + erf(g / sqrt(2))) / 2
+ *          GELU_TANH  g * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2
+ *          RELU       max(g, 0); its derivative is 0 at g = 0 */
+#define GEMM_ACT_SILU 0
+#define GEMM_ACT_GELU 1
+#define GEMM_ACT_GELU_TANH 2
+#define GEMM_ACT_RELU 3
+
+/*
+ * gated_ff -- G = X Wg, U = X Wu, H = act(G) * U in one pass over X.
+ *
+ * X is M x D (tokens x width), the weights map D to F; H, G and U are M x F.
+ * Everything is row-major with leading dimensions in elements.  op_w says how
+ * both weights are stored: GEMM_OP_N as D x F (ldw >= F), GEMM_OP_T as F x D
+ * (ldw >= D, the "out x in" storage of most model files).
+ * dtype: GEMM_DT_F32 or GEMM_DT_BF16, of X, the weights and H.  Products are
+ * summed in FP32; act and the product are computed in FP32 from those sums and
+ * H is rounded once.  GEMM_DT_F32 has FP32 accuracy.  A non-finite input gives NaN
+ * in FP32 (as in GEMM_MODE_TF32X3); in BF16 Inf and NaN follow IEEE rules.
+ * G, U: the sums for a later backward pass, or both NULL.  They are FP32 in
+ * either dtype: rounded to BF16 they would put an error of their own, as
+ * large as a BF16 result's rounding, into every gradient.  H may be NULL when
+ * G and U are given.
+ * M, D, F >= 0; D = 0 gives zeros.  Outputs must not overlap inputs.
+ * workspace: gated_ff_workspace() bytes, 256-byte aligned, or NULL for the
+ * library's per-device buffer (with the rules of gemm_f32_ex).
+ */
+GEMM_API int gated_ff(int dtype, int act, int op_w, int64_t M, int64_t D, int64_t F,
+                      const void *X, int64_t ldx, const void *Wg, int64_t ldwg,
+                      const void *Wu, int64_t ldwu, void *H, int64_t ldh, float *G, int64_t ldg,
+                      float *U, int64_t ldu, void *workspace, size_t ws_bytes,
+                      cudaStream_t stream);
+
+/*
+ * gated_ff_backward -- the gradients of gated_ff given dH (M x F):
+ *     dG = dH * U * act'(G)       dU = dH * act(G)
+ *     dX = dG Wg^T + dU Wu^T      dWg = X^T dG      dWu = X^T dU
+ * G and U (FP32) are those gated_ff saved.  dWg and dWu are stored as the weights
+ * are (op_w).  dX, or dWg and dWu together, may be NULL: not computed (X is
+ * then only needed for dWg and dWu, the weights only for dX).  In BF16, dG
+ * and dU are rounded to BF16 before the products, which are summed in FP32.
+ * The gradients are written, not added to.  M = 0 gives zero dWg and dWu,
+ * F = 0 zero dX.
+ */
+GEMM_API int gated_ff_backward(int dtype, int act, int op_w, int64_t M, int64_t D, int64_t F,
+                               const void *dH, int64_t lddh, const void *X, int64_t ldx,
+                               const void *Wg, int64_t ldwg, const void *Wu, int64_t ldwu,
+                               const float *G, int64_t ldg, const float *U, int64_t ldu,
+                               void *dX, int64_t lddx, void *dWg, int64_t lddwg, void *dWu,
+                               int64_t lddwu, void *workspace, size_t ws_bytes,
+                               cudaStream_t stream);
+
+/*
+ * gated_ff_workspace -- scratch bytes that cover a gated_ff (backward = 0)
+ * or gated_ff_backward (1) call of these sizes.  aligned = 1: every matrix
+ * is 16-byte aligned with a leading dimension that is a multiple of 16
+ * bytes; 0: any.  Host only.
+ */
+GEMM_API int gated_ff_workspace(int backward, int dtype, int op_w, int64_t M, int64_t D,
+                                int64_t F, int aligned, uint64_t *bytes);
+
+/*
+ * q4_matmul -- Y = X W^T with 4-bit weights, for a few tokens:
+ *     Y(m,n) = sum_k X(m,k) * s(n, k / group) * (q(n,k) - z(n, k / group))
+ * X is M x K and Y is M x N (row-major, leading dimensions in elements).
+ * Q: N rows of 4-bit codes 0..15, ldq BYTES apart (ldq >= (K + 1) / 2), two
+ * codes a byte, q(n, 2i) in the low half and q(n, 2i + 1) in the high half
+ * of byte i.  S, Z: N x ceil(K / group) scales and zero points, contiguous,
+ * of the same dtype as X and Y; Z may be NULL (every zero point 8).
+ * group: 32, 64, 128 or 256.  dtype F32 or BF16; products are summed in
+ * FP32 and exact to FP32 in F32.  The weights are read once for every 8
+ * tokens (BF16) or 2 (F32): meant for M up to a few dozen.
+ */
+GEMM_API int q4_matmul(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+                       const void *Q, int64_t ldq, const void *S, const void *Z, int group,
+                       void *Y, int64_t ldy, cudaStream_t stream);
+
+/*
+ * q4_gated -- H = act(X Wg^T) * (X Wu^T), both matrices N x K in the format
+ * of q4_matmul with one group size: the gated block for a few tokens, in one
+ * launch.  Zg and Zu are given together or both NULL.
+ */
+GEMM_API int q4_gated(int dtype, int act, int64_t M, int64_t N, int64_t K, const void *X,
+                      int64_t ldx, const void *Qg, int64_t ldqg, const void *Sg, const void *Zg,
+                      const void *Qu, int64_t ldqu, const void *Su, const void *Zu, int group,
+                      void *H, int64_t ldh, cudaStream_t stream);
+
+/*
+ * grad_norm_clip -- norm = sqrt(sum of all squares) over `count` tensors,
+ * and out_i = grad_i * min(1, max_norm / (norm + 1e-6)).
+ * grads, outs: HOST arrays of `count` device pointers; sizes: HOST array of
+ * element counts (>= 0); dtypes: HOST array of GEMM_DT_*.  The arrays are
+ * read before the call returns.  outs == NULL: only the norm.  outs[i] may
+ * equal grads[i] (in place); otherwise outputs overlap no input.  Tensors
+ * need only be aligned to their element size.
+ * norm: device pointer to one float, written with the norm before clipping
+ * (0 for no elements; Inf or NaN as the sum of squares gives it, and the
+ * outputs follow the formula).  The order of the sums is fixed: equal calls
+ * give equal bits.
+ * workspace: grad_norm_clip_workspace(count) bytes, 256-byte aligned, or
+ * NULL for the library's per-device buffer.
+ */
+GEMM_API int grad_norm_clip(int64_t count, const int *dtypes, const void *const *grads,
+                            void *const *outs, const int64_t *sizes, float max_norm,
+                            float *norm, void *workspace, size_t ws_bytes, cudaStream_t stream);
+GEMM_API uint64_t grad_norm_clip_workspace(int64_t count);
+
 /* Frees the library's per-device workspace buffers.  Call with no library
  * work in flight. */
 GEMM_API void gemm_shutdown(void);

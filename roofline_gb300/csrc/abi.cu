@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "ff.cuh"
 
 namespace gg {
 
@@ -86,6 +87,12 @@ int check_args(int64_t M, int64_t N, int64_t K, const float *A, int64_t lda, con
   return GEMM_OK;
 }
 
+thread_local cudaEvent_t t_prof_before = nullptr;
+thread_local cudaEvent_t t_prof_after = nullptr;
+thread_local unsigned long long *t_prof_stamps = nullptr;
+
+}  // namespace
+
 int current_device(int *dev) {
   if (cudaGetDevice(dev) != cudaSuccess) {
     cudaGetLastError();
@@ -117,12 +124,6 @@ int library_workspace(int dev, size_t need, void **out) {
 }
 
 int to_status(cudaError_t e) { return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA; }
-
-thread_local cudaEvent_t t_prof_before = nullptr;
-thread_local cudaEvent_t t_prof_after = nullptr;
-thread_local unsigned long long *t_prof_stamps = nullptr;
-
-}  // namespace
 
 void profile_mark_before(cudaStream_t s) {
   if (t_prof_before) cudaEventRecord(t_prof_before, s);

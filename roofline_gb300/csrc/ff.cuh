@@ -1,0 +1,73 @@
+// Shared by the feed-forward operators (ff.cu, q4.cu, clip.cu): element types
+// and the activations with their derivatives.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace gg {
+
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(bf16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ bf16 from_f32<bf16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+// act(g) (formulas in gb300_gemm.h).  FAST: exponentials by __expf and
+// quotients by __fdividef, a few units of 2^-22 off: for results that are
+// rounded to BF16 (2^-8).
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float x) {
+  return FAST ? __fdividef(1.0f, 1.0f + __expf(-x)) : 1.0f / (1.0f + expf(-x));
+}
+
+template <bool FAST>
+__device__ __forceinline__ float act_value(float g, int act) {
+  if (act == GEMM_ACT_SILU) return g * sigmoid<FAST>(g);
+  if (act == GEMM_ACT_RELU) return g > 0.0f ? g : (g != g ? g : 0.0f);
+  if (act == GEMM_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678f));
+  // (1 + tanh(u)) / 2 = sigmoid(2u)
+  return g * sigmoid<FAST>(2.0f * 0.79788456f * (g + 0.044715f * g * g * g));
+}
+
+// act(g) and act'(g).
+template <bool FAST>
+__device__ __forceinline__ void act_both(float g, int act, float &a, float &d) {
+  if (act == GEMM_ACT_SILU) {
+    const float s = sigmoid<FAST>(g);
+    a = g * s;
+    d = s * (1.0f + g * (1.0f - s));
+  } else if (act == GEMM_ACT_RELU) {
+    a = g > 0.0f ? g : (g != g ? g : 0.0f);
+    d = g > 0.0f ? 1.0f : 0.0f;
+  } else if (act == GEMM_ACT_GELU) {
+    const float p = 0.5f * (1.0f + erff(g * 0.70710678f));
+    a = g * p;
+    d = p + g * 0.39894228f * (FAST ? __expf(-0.5f * g * g) : expf(-0.5f * g * g));
+  } else {
+    const float s = sigmoid<FAST>(2.0f * 0.79788456f * (g + 0.044715f * g * g * g));
+    a = g * s;
+    d = s + 2.0f * g * s * (1.0f - s) * 0.79788456f * (1.0f + 0.134145f * g * g);
+  }
+}
+
+inline bool dtype_known(int d) { return d == GEMM_DT_F32 || d == GEMM_DT_BF16; }
+inline bool act_known(int a) { return a >= GEMM_ACT_SILU && a <= GEMM_ACT_RELU; }
+inline size_t dtype_size(int d) { return d == GEMM_DT_F32 ? 4 : 2; }
+
+// abi.cu
+int current_device(int *dev);
+int library_workspace(int dev, size_t need, void **out);
+int to_status(cudaError_t e);
+
+}  // namespace gg

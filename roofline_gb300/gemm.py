@@ -53,7 +53,9 @@ EXPORTED = ["gemm_f32", "gemm_f32_ex", "gemm_f32_plan", "gemm_f32_op", "gemm_f32
             "gemm_device_info", "gemm_strerror", "gemm_check_status", "gemm_shutdown",
             "gemm_abi_version", "gemm_set_profile_events", "gemm_set_profile_stamps",
             "gemm_f32_splitk_noalloc",
-            "fp32_fma_peak", "fp32_fma_peak_sink_floats"]
+            "fp32_fma_peak", "fp32_fma_peak_sink_floats",
+            "gated_ff", "gated_ff_backward", "gated_ff_workspace", "q4_matmul", "q4_gated",
+            "grad_norm_clip", "grad_norm_clip_workspace"]
 
 # most row blocks gemm_f32_host pipelines
 HOST_MAX_BLOCKS = 64
@@ -170,6 +172,20 @@ def load(path: str | None = None):
         lib.fp32_fma_peak.restype = i32
         lib.fp32_fma_peak_sink_floats.argtypes = []
         lib.fp32_fma_peak_sink_floats.restype = i64
+        sz, m = ctypes.c_size_t, [vp, i64]  # m: a matrix and its leading dimension
+        lib.gated_ff.argtypes = [i32, i32, i32, i64, i64, i64] + 6 * m + [vp, sz, vp]
+        lib.gated_ff_backward.argtypes = [i32, i32, i32, i64, i64, i64] + 9 * m + [vp, sz, vp]
+        lib.gated_ff_workspace.argtypes = [i32, i32, i32, i64, i64, i64, i32,
+                                           ctypes.POINTER(ctypes.c_uint64)]
+        lib.q4_matmul.argtypes = [i32, i64, i64, i64] + 2 * m + [vp, vp, i32] + m + [vp]
+        lib.q4_gated.argtypes = [i32, i32, i64, i64, i64] + m + 2 * (m + [vp, vp]) + [i32] + m + \
+            [vp]
+        lib.grad_norm_clip.argtypes = [i64, vp, vp, vp, vp, f32, vp, vp, sz, vp]
+        for name in ("gated_ff", "gated_ff_backward", "gated_ff_workspace", "q4_matmul",
+                     "q4_gated", "grad_norm_clip"):
+            getattr(lib, name).restype = i32
+        lib.grad_norm_clip_workspace.argtypes = [i64]
+        lib.grad_norm_clip_workspace.restype = ctypes.c_uint64
         # the structures above mirror this version of the header
         if lib.gemm_abi_version() != ABI_VERSION:
             raise RuntimeError(f"{p} reports ABI version {lib.gemm_abi_version()}, this binding "

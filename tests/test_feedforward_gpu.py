@@ -1,0 +1,473 @@
+"""The feed-forward operators on the GPU against their formulas in 64 bits,
+at the sizes, strides and values where they can go wrong.  The tolerances are
+the bounds of ff_reference."""
+import math
+
+import pytest
+import torch
+
+from tests import ff_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+ACTS = ["silu", "gelu", "gelu_tanh", "relu"]
+
+
+@pytest.fixture(scope="module")
+def ff():
+    from roofline_gb300 import build, feedforward
+    build.build()
+    return feedforward
+
+
+def _mat(g, rows, cols, dt, scale=1.0, pad=0, off=0):
+    """rows x cols, cut out of a buffer `pad` columns wider from column `off` on."""
+    t = torch.randn((rows, cols + pad), generator=g) * scale
+    return t.to(dt).cuda()[:, off:off + cols]
+
+
+def _weight(g, D, F, dt, order, pad=0, off=0):
+    s = max(D, 1) ** -0.5
+    return _mat(g, F, D, dt, s, pad, off).t() if order == "oi" else _mat(g, D, F, dt, s, pad, off)
+
+
+def _case(seed, M, D, F, dt, order, pad=0, off=0):
+    g = torch.Generator().manual_seed(seed)
+    return (_mat(g, M, D, dt, 1.0, pad, off), _weight(g, D, F, dt, order, pad, off),
+            _weight(g, D, F, dt, order, pad, off), _mat(g, M, F, dt, 1.0, pad, off))
+
+
+def _check_forward(ff, X, Wg, Wu, act):
+    want = ref.forward(X, Wg, Wu, act)
+    H, G, U = ff.gated_ff(X, Wg, Wu, act=act, save=True)
+    H2 = ff.gated_ff(X, Wg, Wu, act=act)
+    torch.cuda.synchronize()
+    for name, t in (("H", H), ("G", G), ("U", U), ("H", H2)):
+        assert ref.worst(t, want[name]) <= 1.0, name
+    return G, U
+
+
+def _check_backward(ff, dH, X, Wg, Wu, G, U, act):
+    got = ff.gated_ff_backward(dH, X, Wg, Wu, G, U, act=act)
+    torch.cuda.synchronize()
+    want = ref.backward(dH, X, Wg, Wu, G, U, act)
+    for name, t in zip(("dX", "dWg", "dWu"), got):
+        assert ref.worst(t, want[name]) <= 1.0, name
+
+
+SIZES = [(1, 1, 1), (1, 64, 64), (2, 8, 16), (3, 5, 7), (17, 100, 33), (31, 129, 127),
+         (64, 64, 64), (128, 256, 128), (129, 72, 200), (257, 136, 264), (300, 520, 130),
+         (1, 1000, 515), (8, 515, 1000), (33, 2048, 96), (700, 40, 300), (1030, 260, 1032)]
+
+
+@pytest.mark.parametrize("order", ["oi", "io"])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", SIZES)
+def test_forward_and_backward(ff, size, dt, order):
+    act = ACTS[sum(size) % 4]
+    X, Wg, Wu, dH = _case(sum(size), *size, dt, order)
+    G, U = _check_forward(ff, X, Wg, Wu, act)
+    _check_backward(ff, dH, X, Wg, Wu, G, U, act)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_activations(ff, dt, act):
+    """Every activation over gate values from deep in one tail to deep in the other."""
+    g = torch.Generator().manual_seed(5)
+    D, F, M = 16, 160, 70
+    X = torch.zeros(M, D)
+    X[:, 0] = torch.linspace(-30, 30, M)  # G(i, j) = x_i * w_j: from -90 to 90
+    X[:, 1:] = torch.randn((M, D - 1), generator=g) * 0.1
+    Wg = torch.randn((D, F), generator=g) * 0.1
+    Wg[0] = torch.linspace(-3, 3, F)
+    Wu = torch.randn((D, F), generator=g)
+    X, Wg, Wu = (t.to(dt).cuda() for t in (X, Wg, Wu))
+    dH = torch.randn((M, F), generator=g).to(dt).cuda()
+    G, U = _check_forward(ff, X, Wg, Wu, act)
+    _check_backward(ff, dH, X, Wg, Wu, G, U, act)
+
+
+@pytest.mark.parametrize("order", ["oi", "io"])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("pad,off", [(8, 0), (8, 8), (3, 0), (5, 1), (16, 3)])
+@pytest.mark.parametrize("size", [(5, 96, 72), (130, 200, 136)])
+def test_strided_and_misaligned(ff, size, pad, off, dt, order):
+    X, Wg, Wu, dH = _case(pad + off, *size, dt, order, pad, off)
+    G, U = _check_forward(ff, X, Wg, Wu, "silu")
+    _check_backward(ff, dH, X, Wg, Wu, G, U, "silu")
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M", [2, 200])
+def test_output_rows_of_wider_buffers_are_left_alone(ff, M, dt):
+    """H goes into columns of a wider buffer; what is around them stays."""
+    D, F = 72, 131
+    X, Wg, Wu, _ = _case(9, M, D, F, dt, "oi")
+    wide = torch.full((M + 1, F + 9), 7.0, dtype=dt, device="cuda")
+    ff.gated_ff(X, Wg, Wu, out=wide[:M, 4:4 + F])
+    torch.cuda.synchronize()
+    assert ref.worst(wide[:M, 4:4 + F], ref.forward(X, Wg, Wu, "silu")["H"]) <= 1.0
+    wide[:M, 4:4 + F] = 7.0
+    assert bool((wide == 7.0).all())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_empty_extents(ff, dt):
+    for M, D, F in ((0, 8, 8), (4, 8, 0), (4, 0, 8), (0, 0, 0)):
+        X, Wg, Wu, dH = _case(1, M, D, F, dt, "io")
+        H, G, U = ff.gated_ff(X, Wg, Wu, save=True)
+        dX, dWg, dWu = ff.gated_ff_backward(dH, X, Wg, Wu, G, U)
+        torch.cuda.synchronize()
+        for t, shape in ((H, (M, F)), (dX, (M, D)), (dWg, (D, F)), (dWu, (D, F))):
+            assert tuple(t.shape) == shape and not bool(t.float().abs().sum())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_nan_and_inf(ff, dt):
+    """A NaN in a token's row reaches that row only; an Inf in X gives no finite G in its
+    row (Inf or NaN), and leaves the others alone."""
+    X, Wg, Wu, dH = _case(2, 140, 80, 96, dt, "oi")
+    X = X.clone()
+    X[3, 5] = math.nan
+    X[130, 0] = math.inf
+    H, G, U = ff.gated_ff(X, Wg, Wu, save=True)
+    torch.cuda.synchronize()
+    rows = torch.ones(140, dtype=torch.bool)
+    rows[3] = rows[130] = False
+    clean = X.clone()
+    clean[~rows.cuda()] = 0
+    want = ref.forward(clean, Wg, Wu, "silu")
+    for name, t in (("H", H), ("G", G), ("U", U)):
+        assert ref.worst(t[rows.cuda()], tuple(x[rows] for x in want[name])) <= 1.0
+    assert bool(G[3].isnan().all()) and bool(H[3].isnan().all())
+    assert not bool(G[130].isfinite().any())
+
+
+def test_large_and_small_values_f32(ff):
+    """FP32 inputs near the ends of the range: what is representable comes out."""
+    g = torch.Generator().manual_seed(8)
+    X = torch.randn((40, 64), generator=g) * 1e18
+    Wg = torch.randn((64, 48), generator=g) * 1e-18
+    Wu = torch.randn((64, 48), generator=g) * 1e-15
+    X[0, 0], Wg[0, 0], Wu[0, 0] = 3.4e38, 1e-25, 1e-28
+    X, Wg, Wu = X.cuda(), Wg.cuda(), Wu.cuda()
+    _check_forward(ff, X, Wg, Wu, "gelu")
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_some_gradients_only(ff, dt):
+    X, Wg, Wu, dH = _case(4, 90, 64, 80, dt, "io")
+    _, G, U = ff.gated_ff(X, Wg, Wu, save=True)
+    full = ff.gated_ff_backward(dH, X, Wg, Wu, G, U)
+    dX, none1, none2 = ff.gated_ff_backward(dH, X, Wg, Wu, G, U, need_dw=False)
+    none3, dWg, dWu = ff.gated_ff_backward(dH, X, Wg, Wu, G, U, need_dx=False)
+    torch.cuda.synchronize()
+    assert none1 is None and none2 is None and none3 is None
+    for a, b in zip(full, (dX, dWg, dWu)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_gradient_against_differences(ff, act):
+    """The kernel's gradients against central differences of the kernel's own
+    forward pass in FP32.  The difference of the loss L = sum dH * H over 2h is
+    off by the bounds of H at both points over 2h, and by what the difference
+    of the 64-bit formula with the same h is off."""
+    M, D, F, h = 24, 40, 48, 2.0 ** -5
+    X, Wg, Wu, dH = _case(11, M, D, F, F32, "io")
+    _, G, U = ff.gated_ff(X, Wg, Wu, act=act, save=True)
+    grads = ff.gated_ff_backward(dH, X, Wg, Wu, G, U, act=act)
+    g = torch.Generator().manual_seed(12)
+    for k in range(3):
+        v = torch.randn(grads[k].shape, generator=g).cuda()
+        v /= v.norm()
+        num = num64 = slack = 0.0
+        for sign in (1.0, -1.0):
+            at = [X, Wg, Wu]
+            at[k] = at[k] + sign * h * v
+            H = ff.gated_ff(*at, act=act).double()
+            val, e = ref.forward(*at, act)["H"]
+            num += sign * float((dH.double() * H).sum()) / (2 * h)
+            num64 += sign * float((dH.double().cpu() * val).sum()) / (2 * h)
+            slack += float((dH.double().cpu().abs() * e).sum()) / (2 * h)
+        want = float((grads[k].double() * v.double()).sum())
+        exact = ref.backward(dH, X, Wg, Wu, G, U, act)[("dX", "dWg", "dWu")[k]]
+        true = float((exact[0] * v.double().cpu()).sum())
+        own = float((exact[1] * v.double().cpu().abs()).sum())
+        # v rounded into at[k] moves the point by 2^-24 of it: within slack's 1e-5
+        assert abs(num - want) <= abs(num64 - true) + slack + own
+        # and the check has teeth: that slack is well under the gradient itself
+        assert abs(num64 - true) + slack + own <= 0.5 * float(grads[k].norm())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_own_stream_and_workspace(ff, dt):
+    """Inputs made on one stream, the call on another, its own workspace; too small a one
+    is refused; repeated calls give the same bits."""
+    from roofline_gb300 import gemm
+    M, D, F = 150, 77, 90
+    X, Wg, Wu, dH = _case(6, M, D, F, dt, "oi")
+    code = ff.DT_F32 if dt == F32 else ff.DT_BF16
+    _, G0, U0 = ff.gated_ff(X, Wg, Wu, save=True)
+    first = ff.gated_ff_backward(dH, X, Wg, Wu, G0, U0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    need = [max(ff.gated_ff_workspace(M, D, F, code, gemm.OP_T, b), 256) for b in (False, True)]
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in need]
+    H, G, U = ff.gated_ff(X, Wg, Wu, save=True, stream=side, workspace=ws[0])
+    got = ff.gated_ff_backward(dH, X, Wg, Wu, G, U, stream=side, workspace=ws[1])
+    torch.cuda.synchronize()
+    assert torch.equal(G, G0) and torch.equal(U, U0)
+    for a, b in zip(first, got):
+        assert torch.equal(a, b)
+    with pytest.raises(gemm.GemmError):
+        ff.gated_ff_backward(dH, X, Wg, Wu, G, U, workspace=ws[1][:256])
+    assert gemm.check_status() == gemm.OK
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_captured_in_a_graph(ff, dt):
+    X, Wg, Wu, dH = _case(6, 200, 128, 144, dt, "oi")
+    H, G, U = ff.gated_ff(X, Wg, Wu, save=True)
+    want = ff.gated_ff_backward(dH, X, Wg, Wu, G, U)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        H2, G2, U2 = ff.gated_ff(X, Wg, Wu, save=True)
+        got = ff.gated_ff_backward(dH, X, Wg, Wu, G2, U2)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(H, H2)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ 4-bit products
+
+def _quant(g, N, K, group, dt, zeros, pad=0):
+    """Random codes (all 16 values), scales of both signs, zero points off the grid too."""
+    q = torch.randint(0, 256, (N, (K + 1) // 2 + pad), generator=g, dtype=torch.uint8)
+    groups = -(-K // group)
+    s = (torch.randn((N, groups), generator=g) * max(K, 1) ** -0.5).to(dt).cuda()
+    z = (torch.rand((N, groups), generator=g) * 15).to(dt).cuda() if zeros else None
+    return q.cuda()[:, :(K + 1) // 2], s, z
+
+
+Q4_SIZES = [(1, 1, 1), (1, 8, 32), (1, 16, 64), (2, 3, 5), (3, 17, 33), (1, 64, 127),
+            (4, 100, 256), (5, 33, 300), (7, 130, 1025), (8, 256, 512), (9, 65, 640),
+            (16, 48, 2048), (17, 96, 1000), (33, 40, 96), (1, 1031, 4096), (2, 40, 9001)]
+
+
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("zeros", [False, True], ids=["z8", "zeros"])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", Q4_SIZES)
+def test_q4(ff, size, dt, zeros, group):
+    M, N, K = size
+    g = torch.Generator().manual_seed(M + N + K + group)
+    X = _mat(g, M, K, dt)
+    w, u = _quant(g, N, K, group, dt, zeros), _quant(g, N, K, group, dt, zeros)
+    Y = ff.q4_matmul(X, w[0], w[1], zeros=w[2], group=group)
+    act = ACTS[(M + N) % 4]
+    H = ff.q4_gated(X, w[0], w[1], u[0], u[1], zeros_g=w[2], zeros_u=u[2], group=group, act=act)
+    torch.cuda.synchronize()
+    assert ref.worst(Y, ref.q4_rounded(X, *w, group)) <= 1.0
+    assert ref.worst(H, ref.q4_gated(X, w, u, group, act)) <= 1.0
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("pad,off", [(0, 1), (1, 0), (3, 1), (16, 0), (15, 5)])
+@pytest.mark.parametrize("K", [96, 513])
+def test_q4_strides(ff, K, pad, off, dt):
+    """Rows of codes any number of bytes apart, X and Y cut out of wider buffers."""
+    M, N, group = 5, 70, 64
+    g = torch.Generator().manual_seed(pad + off + K)
+    X = _mat(g, M, K, dt, 1.0, pad + off, off)
+    q, s, z = _quant(g, N, K, group, dt, True, pad)
+    wide = torch.full((M, N + pad + 2), 7.0, dtype=dt, device="cuda")
+    ff.q4_matmul(X, q, s, zeros=z, group=group, out=wide[:, 1:1 + N])
+    torch.cuda.synchronize()
+    assert ref.worst(wide[:, 1:1 + N], ref.q4_rounded(X, q, s, z, group)) <= 1.0
+    wide[:, 1:1 + N] = 7.0
+    assert bool((wide == 7.0).all())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_q4_empty_and_nan(ff, dt):
+    g = torch.Generator().manual_seed(1)
+    q, s, z = _quant(g, 20, 100, 32, dt, True)
+    assert ff.q4_matmul(_mat(g, 0, 100, dt), q, s, zeros=z, group=32).shape == (0, 20)
+    # K = 0: zeros
+    q0 = torch.zeros((20, 0), dtype=torch.uint8, device="cuda")
+    s0 = torch.zeros((20, 0), dtype=dt, device="cuda")
+    y = ff.q4_matmul(_mat(g, 3, 0, dt), q0, s0, group=32)
+    torch.cuda.synchronize()
+    assert y.shape == (3, 20) and not bool(y.any())
+    # a NaN in one token reaches its row only; the last code of an odd K is not read as a weight
+    X = _mat(g, 12, 99, dt).clone()
+    X[4, 7] = math.nan
+    q, s, z = _quant(g, 20, 99, 32, dt, False)
+    Y = ff.q4_matmul(X, q, s, group=32)
+    torch.cuda.synchronize()
+    rows = [i for i in range(12) if i != 4]
+    X[4] = 0
+    val, e = ref.q4_rounded(X, q, s, None, 32)
+    assert ref.worst(Y[rows], (val[rows], e[rows])) <= 1.0
+    assert bool(Y[4].isnan().all())
+
+
+def test_q4_on_another_stream_and_in_a_graph(ff):
+    g = torch.Generator().manual_seed(1)
+    X = _mat(g, 1, 512, BF16)
+    q, s, z = _quant(g, 300, 512, 128, BF16, True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a = ff.q4_matmul(X, q, s, zeros=z, stream=side)
+    b = ff.q4_matmul(X, q, s, zeros=z)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c = ff.q4_matmul(X, q, s, zeros=z)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, c)
+
+
+# ------------------------------------------------------------------ norm and clipping
+
+def _grads(g, specs, scale=0.1):
+    """Tensors given as (size, dtype, offset of the first element in its buffer)."""
+    out = []
+    for n, dt, off in specs:
+        t = (torch.randn(n + off, generator=g) * scale).to(dt).cuda()
+        out.append(t[off:])
+    return out
+
+
+def _norm64(ts):
+    return math.sqrt(sum(float((t.double() ** 2).sum()) for t in ts))
+
+
+def _check_clip(ts, outs, norm, max_norm):
+    """norm: squares and sums of a thread's few values in FP32 (2^-24 each, at most 64 of
+    them, half of that after the root), the rest in 64 bits, one rounding: 2^-18.  Outputs:
+    the norm's error, two roundings of the factor, one product, one rounding."""
+    n64 = _norm64(ts)
+    assert abs(float(norm) - n64) <= 2.0 ** -18 * n64
+    c = min(1.0, max_norm / (n64 + 1e-6))
+    for t, o in zip(ts, outs):
+        want = t.double() * c
+        tol = 2.0 ** -17 + ref.ROUND[t.dtype]
+        # a result below the normal range is rounded to a multiple of 2^-149 (FP32)
+        # or 2^-133 (BF16)
+        tiny = 2.0 ** -149 if t.dtype == F32 else 2.0 ** -133
+        assert bool(((o.double() - want).abs() <= tol * want.abs() + tiny).all())
+
+
+SPECS = {
+    "one": [(1, F32, 0)],
+    "small": [(5, F32, 0), (0, F32, 0), (7, BF16, 1), (1, BF16, 0), (0, BF16, 0)],
+    "odd offsets": [(1000 + 37 * i, F32 if i % 3 else BF16, i % 9) for i in range(30)],
+    "large and small": [(3_000_001, BF16, 0), (3, F32, 1), (1_000_003, F32, 3), (1, BF16, 5)],
+    "many": [(1 + (i * 7919) % 997, BF16 if i % 2 else F32, i % 4) for i in range(2500)],
+}
+
+
+@pytest.mark.parametrize("max_norm", [0.5, 1e6, 0.0])
+@pytest.mark.parametrize("name", list(SPECS))
+def test_clip(ff, name, max_norm):
+    g = torch.Generator().manual_seed(len(name))
+    ts = _grads(g, SPECS[name])
+    before = [t.clone() for t in ts]
+    outs = [torch.full_like(t, 9.0) for t in ts]
+    norm = ff.clip_grad_norm(ts, max_norm, out=outs)
+    only = ff.grad_norm(ts)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ts, before))
+    assert float(norm) == float(only)
+    _check_clip(before, outs, norm, max_norm)
+    # in place: the same bits
+    norm2 = ff.clip_grad_norm(ts, max_norm)
+    torch.cuda.synchronize()
+    assert float(norm2) == float(norm)
+    assert all(torch.equal(a, b) for a, b in zip(ts, outs))
+
+
+def test_clip_neighbours_are_left_alone(ff):
+    """Tensors next to one another in one buffer, inputs and outputs aligned differently."""
+    g = torch.Generator().manual_seed(3)
+    for dt in (F32, BF16):
+        flat = torch.randn(5000, generator=g).to(dt).cuda()
+        dest = torch.full((5003,), 9.0, dtype=dt, device="cuda")
+        cuts = [0, 1, 9, 10, 1033, 1040, 3001, 4999]
+        ts = [flat[a:b] for a, b in zip(cuts, cuts[1:])]
+        outs = [dest[a + 3:b + 3] for a, b in zip(cuts, cuts[1:])]
+        norm = ff.clip_grad_norm(ts, 1.0, out=outs)
+        torch.cuda.synchronize()
+        _check_clip(ts, outs, norm, 1.0)
+        assert bool((dest[:3] == 9.0).all()) and float(dest[5002]) == 9.0
+
+
+def test_clip_no_tensors_and_empty_ones(ff):
+    norm = ff.clip_grad_norm([], 1.0)
+    empty = ff.clip_grad_norm([torch.zeros(0, device="cuda")], 1.0)
+    zero = [torch.zeros(1000, device="cuda")]
+    nz = ff.clip_grad_norm(zero, 1.0)
+    torch.cuda.synchronize()
+    assert float(norm) == 0.0 and float(empty) == 0.0 and float(nz) == 0.0
+    assert not bool(zero[0].any())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_clip_not_finite(ff, dt):
+    """Inf: the norm is Inf, the factor 0 (Inf * 0 = NaN at the Inf); NaN: all NaN."""
+    for bad in (math.inf, math.nan):
+        t = torch.ones(2000, dtype=dt, device="cuda")
+        t[1234] = bad
+        norm = ff.clip_grad_norm([t], 1.0)
+        torch.cuda.synchronize()
+        if bad == math.inf:
+            assert float(norm) == math.inf
+            assert bool(t[1234].isnan()) and int(t.isnan().sum()) == 1 and float(t[0]) == 0.0
+        else:
+            assert math.isnan(float(norm)) and bool(t.isnan().all())
+
+
+def test_clip_range(ff):
+    """Squares beyond FP32's range: 1e25 squared overflows a float, 1e-30 squared underflows."""
+    for v in (1e25, 1e-30):
+        t = torch.full((3000,), v, device="cuda")
+        norm = ff.grad_norm([t])
+        torch.cuda.synchronize()
+        want = float(t[0].double()) * math.sqrt(3000.0)
+        assert abs(float(norm) - want) <= 2.0 ** -18 * want
+
+
+def test_clip_stream_graph_and_workspace(ff):
+    from roofline_gb300 import gemm
+    g = torch.Generator().manual_seed(3)
+    ts = _grads(g, SPECS["odd offsets"])
+    outs = [torch.empty_like(t) for t in ts]
+    norm = ff.clip_grad_norm(ts, 0.25, out=outs)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ws = torch.empty(int(gemm.load().grad_norm_clip_workspace(len(ts))), dtype=torch.uint8,
+                     device="cuda")
+    outs2 = [torch.empty_like(t) for t in ts]
+    norm2 = ff.clip_grad_norm(ts, 0.25, out=outs2, stream=side, workspace=ws)
+    torch.cuda.synchronize()
+    assert float(norm) == float(norm2) and all(torch.equal(a, b) for a, b in zip(outs, outs2))
+    with pytest.raises(gemm.GemmError):
+        ff.clip_grad_norm(ts, 0.25, out=outs2, workspace=ws[:64])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm3 = ff.clip_grad_norm(ts, 0.25, out=outs2)
+    for o in outs2:
+        o.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert float(norm) == float(norm3) and all(torch.equal(a, b) for a, b in zip(outs, outs2))
