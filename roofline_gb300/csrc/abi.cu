@@ -9,7 +9,7 @@
 #include <mutex>
 
 #include "common.cuh"
-#include "ff.cuh"
+#include "ff_tc.cuh"
 
 namespace gg {
 
@@ -440,7 +440,9 @@ int gemm_check_status(cudaStream_t stream) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
-  return tc_read_and_clear_status(stream);
+  const int ff = ff_read_and_clear_status();
+  const int tc = tc_read_and_clear_status(stream);
+  return tc != GEMM_OK ? tc : ff;
 }
 
 void gemm_shutdown(void) {

@@ -1,88 +1,9 @@
 // The gated feed-forward block and its gradients: argument checks, workspace
 // and the launches (include/gb300_gemm.h, gated_ff and gated_ff_backward).
-#include "ff.cuh"
+#include "ff_tc.cuh"
 
 namespace gg {
 namespace {
-
-// C(i,j) = sum_k A(i,k) B(k,j) (+ sum_k A2(i,k) B2(k,j)); GATED: act of the
-// first sum times the second, whose A is the first's.  Element strides.
-struct Operand {
-  const void *p;
-  int64_t rs, cs;
-};
-struct SimpleArgs {
-  int64_t M, N, K;
-  int act;
-  Operand a, b, a2, b2;
-  void *c;
-  float *g, *u;
-  int64_t ldc, ldg, ldu;
-};
-
-// One 16 x 16 tile of C per block through shared memory, one value a thread.
-template <typename T, bool GATED>
-__global__ void __launch_bounds__(256) ff_simple_kernel(SimpleArgs p) {
-  __shared__ float sa[16][17], sb[16][17], sb2[16][17];
-  const int tx = threadIdx.x, ty = threadIdx.y;
-  const int64_t i = (int64_t)blockIdx.y * 16 + ty, j = (int64_t)blockIdx.x * 16 + tx;
-  float s = 0.0f, s2 = 0.0f;
-  const int parts = !GATED && p.a2.p != nullptr ? 2 : 1;
-  for (int part = 0; part < parts; ++part) {
-    const Operand &A = part ? p.a2 : p.a, &B = part ? p.b2 : p.b;
-    for (int64_t k0 = 0; k0 < p.K; k0 += 16) {
-      const int64_t ka = k0 + tx, kb = k0 + ty;
-      sa[ty][tx] = i < p.M && ka < p.K
-                       ? to_f32(static_cast<const T *>(A.p)[i * A.rs + ka * A.cs])
-                       : 0.0f;
-      sb[ty][tx] = j < p.N && kb < p.K
-                       ? to_f32(static_cast<const T *>(B.p)[kb * B.rs + j * B.cs])
-                       : 0.0f;
-      if (GATED)
-        sb2[ty][tx] = j < p.N && kb < p.K
-                          ? to_f32(static_cast<const T *>(p.b2.p)[kb * p.b2.rs + j * p.b2.cs])
-                          : 0.0f;
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        s = fmaf(sa[ty][k], sb[k][tx], s);
-        if (GATED) s2 = fmaf(sa[ty][k], sb2[k][tx], s2);
-      }
-      __syncthreads();
-    }
-  }
-  if (i >= p.M || j >= p.N) return;
-  if (GATED) {
-    if (p.g) p.g[i * p.ldg + j] = s;
-    if (p.u) p.u[i * p.ldu + j] = s2;
-    s = act_value<false>(s, p.act) * s2;
-  }
-  if (p.c) static_cast<T *>(p.c)[i * p.ldc + j] = from_f32<T>(s);
-}
-
-template <typename T, bool GATED>
-cudaError_t launch_simple(const SimpleArgs &p, cudaStream_t s) {
-  if (p.M == 0 || p.N == 0) return cudaSuccess;
-  ff_simple_kernel<T, GATED><<<dim3((unsigned)ceil_div(p.N, 16), (unsigned)ceil_div(p.M, 16)),
-                               dim3(16, 16), 0, s>>>(p);
-  return cudaGetLastError();
-}
-
-// dG = dH * U * act'(G), dU = dH * act(G), each M x F, contiguous.
-template <typename T>
-__global__ void __launch_bounds__(256)
-ff_dgate_kernel(int64_t M, int64_t F, int act, const T *dH, int64_t lddh, const float *G,
-                int64_t ldg, const float *U, int64_t ldu, T *dG, T *dU) {
-  const int64_t n = M * F;
-  for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < n; e += gridDim.x * 256ll) {
-    const int64_t i = e / F, j = e - i * F;
-    const float h = to_f32(dH[i * lddh + j]);
-    float a, d;
-    act_both<false>(G[i * ldg + j], act, a, d);
-    dG[e] = from_f32<T>(h * U[i * ldu + j] * d);
-    dU[e] = from_f32<T>(h * a);
-  }
-}
 
 bool ld_ok(int64_t ld, int64_t width) { return ld >= (width > 1 ? width : 1); }
 uint64_t align256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
@@ -107,12 +28,56 @@ bool matrix_ok(const void *p, int64_t ld, int64_t rows, int64_t cols, int dtype)
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (dtype_size(dtype) - 1)) == 0;
 }
 
-Operand weight(const void *w, int64_t ld, int op_w) {  // as the D x F matrix
-  return op_w == GEMM_OP_N ? Operand{w, ld, 1} : Operand{w, 1, ld};
+// A stored matrix and, once laid out, the operand made of it.
+struct Stored {
+  const void *p;
+  int64_t rows, cols, ld;
+};
+
+int64_t round8(int64_t x) { return (x + 7) / 8 * 8; }
+int planes_of(int dtype) { return dtype == GEMM_DT_F32 ? 3 : 1; }
+uint64_t plane_bytes(int dtype, int64_t rows, int64_t cols) {
+  return align256((uint64_t)planes_of(dtype) * (uint64_t)rows * (uint64_t)round8(cols) * 2);
 }
 
-uint64_t backward_bytes(int dtype, int64_t M, int64_t F) {
-  return 2 * align256((uint64_t)M * (uint64_t)F * dtype_size(dtype));
+// BF16 rows that TMA reads where they are: 16-byte aligned, or only one.
+bool direct(int dtype, const Stored &m) {
+  return dtype == GEMM_DT_BF16 && (reinterpret_cast<uintptr_t>(m.p) & 15) == 0 &&
+         ((m.ld & 7) == 0 || m.rows == 1);
+}
+
+uint64_t pack_bytes(int dtype, const Stored &m) {
+  return direct(dtype, m) ? 0 : plane_bytes(dtype, m.rows, m.cols);
+}
+
+// Collects the matrices of a call: each is used where it is or gets a place
+// in the workspace and a job of the packing pass.
+struct Layout {
+  int dtype;
+  uint8_t *ws;
+  PackJob jobs[kPackJobs];
+  int n = 0;
+
+  // mn_major: the summed index runs down the rows
+  FfOperand operand(const Stored &m, int mn_major) {
+    if (direct(dtype, m))
+      return {static_cast<const bf16 *>(m.p), m.cols, m.rows,
+              m.rows == 1 ? round8(m.cols) : m.ld, 0, mn_major};
+    FfOperand o{reinterpret_cast<const bf16 *>(ws), m.cols, m.rows, round8(m.cols),
+                m.rows * round8(m.cols), mn_major};
+    jobs[n++] = {m.p, m.rows, m.cols, m.ld, reinterpret_cast<bf16 *>(ws), o.ld, o.plane};
+    ws += plane_bytes(dtype, m.rows, m.cols);
+    return o;
+  }
+};
+
+Stored weight(const void *w, int64_t ld, int op_w, int64_t D, int64_t F) {
+  return op_w == GEMM_OP_N ? Stored{w, D, F, ld} : Stored{w, F, D, ld};
+}
+
+cudaError_t zero(void *p, int64_t ld, int64_t rows, int64_t cols, size_t size, cudaStream_t s) {
+  if (!p || rows == 0 || cols == 0) return cudaSuccess;
+  return cudaMemset2DAsync(p, ld * size, 0, cols * size, rows, s);
 }
 
 // The caller's workspace, or the library's.
@@ -123,11 +88,6 @@ int take_workspace(int dev, uint64_t need, void *workspace, size_t ws_bytes, voi
   if (ws_bytes < need) return GEMM_ERR_WORKSPACE_TOO_SMALL;
   *out = workspace;
   return GEMM_OK;
-}
-
-template <typename T>
-int run_forward(const SimpleArgs &p, cudaStream_t stream) {
-  return to_status(launch_simple<T, true>(p, stream));
 }
 
 }  // namespace
@@ -142,8 +102,11 @@ int gated_ff_workspace(int backward, int dtype, int op_w, int64_t M, int64_t D, 
   if (!bytes) return GEMM_ERR_INVALID_ARG;
   const int st = check_sizes(dtype, GEMM_ACT_SILU, op_w, M, D, F);
   if (st != GEMM_OK) return st;
-  (void)aligned;
-  *bytes = backward ? backward_bytes(dtype, M, F) : 0;
+  const bool packed = dtype == GEMM_DT_F32 || !aligned;
+  *bytes = packed ? plane_bytes(dtype, M, D) + 2 * plane_bytes(dtype, op_w == GEMM_OP_N ? D : F,
+                                                               op_w == GEMM_OP_N ? F : D)
+                  : 0;
+  if (backward) *bytes += 2 * plane_bytes(dtype, M, F);
   return GEMM_OK;
 }
 
@@ -168,56 +131,40 @@ int gated_ff(int dtype, int act, int op_w, int64_t M, int64_t D, int64_t F, cons
   int dev = -1;
   st = current_device(&dev);
   if (st != GEMM_OK) return st;
-  (void)ws_bytes;
-  SimpleArgs p{M, F, D, act, {X, ldx, 1}, weight(Wg, ldwg, op_w), {nullptr, 0, 0},
-               weight(Wu, ldwu, op_w), H, G, U, ldh, ldg, ldu};
-  return dtype == GEMM_DT_F32 ? run_forward<float>(p, stream) : run_forward<bf16>(p, stream);
+  const DeviceProps &dp = props_of(dev);
+  if (D == 0) {
+    cudaError_t e = zero(H, ldh, M, F, dtype_size(dtype), stream);
+    if (e == cudaSuccess) e = zero(G, ldg, M, F, 4, stream);
+    if (e == cudaSuccess) e = zero(U, ldu, M, F, 4, stream);
+    return to_status(e);
+  }
+  const Stored x{X, M, D, ldx}, wg = weight(Wg, ldwg, op_w, D, F), wu = weight(Wu, ldwu, op_w, D, F);
+  void *ws = nullptr;
+  st = take_workspace(dev, pack_bytes(dtype, x) + pack_bytes(dtype, wg) + pack_bytes(dtype, wu),
+                      workspace, ws_bytes, &ws);
+  if (st != GEMM_OK) return st;
+  Layout lay{dtype, static_cast<uint8_t *>(ws)};
+  FfProduct p{};
+  p.kind = kFfGated;
+  p.planes = planes_of(dtype);
+  p.act = act;
+  p.M = M;
+  p.N = F;
+  p.K = D;
+  p.a[0] = lay.operand(x, 0);
+  p.b[0] = lay.operand(wg, op_w == GEMM_OP_N);
+  p.b[1] = lay.operand(wu, op_w == GEMM_OP_N);
+  p.c[0] = H;
+  p.ldc = ldh;
+  p.g = G;
+  p.u = U;
+  p.ldg = ldg;
+  p.ldu = ldu;
+  const cudaError_t e = launch_pack(lay.jobs, lay.n, dtype, dp.sm_count, stream);
+  return e == cudaSuccess ? launch_ff_product(p, dp, stream) : to_status(e);
 }
 
 }  // extern "C"
-
-namespace gg {
-namespace {
-
-template <typename T>
-int run_backward(int act, int op_w, int64_t M, int64_t D, int64_t F, const void *dH, int64_t lddh,
-                 const void *X, int64_t ldx, const void *Wg, int64_t ldwg, const void *Wu,
-                 int64_t ldwu, const float *G, int64_t ldg, const float *U, int64_t ldu, void *dX,
-                 int64_t lddx, void *dWg, int64_t lddwg, void *dWu, int64_t lddwu, void *ws,
-                 cudaStream_t s) {
-  T *dG = static_cast<T *>(ws);
-  T *dU = reinterpret_cast<T *>(static_cast<uint8_t *>(ws) +
-                                align256((uint64_t)M * (uint64_t)F * sizeof(T)));
-  cudaError_t e = cudaSuccess;
-  if (M > 0 && F > 0) {
-    const int64_t blocks = ceil_div(M * F, 256);
-    ff_dgate_kernel<T><<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(
-        M, F, act, static_cast<const T *>(dH), lddh, G, ldg, U, ldu, dG, dU);
-    e = cudaGetLastError();
-  }
-  if (e == cudaSuccess && dX) {
-    Operand wg = weight(Wg, ldwg, op_w), wu = weight(Wu, ldwu, op_w);
-    SimpleArgs p{M, D, F, act, {dG, F, 1}, {wg.p, wg.cs, wg.rs}, {dU, F, 1},
-                 {wu.p, wu.cs, wu.rs}, dX, nullptr, nullptr, lddx, 0, 0};
-    e = launch_simple<T, false>(p, s);
-  }
-  for (int k = 0; k < 2 && e == cudaSuccess && dWg; ++k) {
-    void *dW = k ? dWu : dWg;
-    const int64_t ld = k ? lddwu : lddwg;
-    const T *d = k ? dU : dG;
-    const Operand none{nullptr, 0, 0};
-    SimpleArgs p = op_w == GEMM_OP_N
-                       ? SimpleArgs{D, F, M, act, {X, 1, ldx}, {d, F, 1}, none, none, dW,
-                                    nullptr, nullptr, ld, 0, 0}
-                       : SimpleArgs{F, D, M, act, {d, 1, F}, {X, ldx, 1}, none, none, dW,
-                                    nullptr, nullptr, ld, 0, 0};
-    e = launch_simple<T, false>(p, s);
-  }
-  return to_status(e);
-}
-
-}  // namespace
-}  // namespace gg
 
 extern "C" int gated_ff_backward(int dtype, int act, int op_w, int64_t M, int64_t D, int64_t F,
                                  const void *dH, int64_t lddh, const void *X, int64_t ldx,
@@ -245,12 +192,67 @@ extern "C" int gated_ff_backward(int dtype, int act, int op_w, int64_t M, int64_
   int dev = -1;
   st = current_device(&dev);
   if (st != GEMM_OK) return st;
+  const DeviceProps &dp = props_of(dev);
+  const size_t size = dtype_size(dtype);
+  // an empty sum: zeros
+  if (M == 0 || F == 0) {
+    cudaError_t e = zero(dX, lddx, M, D, size, stream);
+    if (e == cudaSuccess) e = zero(dWg, lddwg, wr, wc, size, stream);
+    if (e == cudaSuccess) e = zero(dWu, lddwu, wr, wc, size, stream);
+    return to_status(e);
+  }
+  const Stored x{X, M, D, ldx}, wg = weight(Wg, ldwg, op_w, D, F), wu = weight(Wu, ldwu, op_w, D, F);
+  const uint64_t part = plane_bytes(dtype, M, F);
+  uint64_t need = 2 * part;
+  if (dX) need += pack_bytes(dtype, wg) + pack_bytes(dtype, wu);
+  if (dWg) need += pack_bytes(dtype, x);
   void *ws = nullptr;
-  st = take_workspace(dev, backward_bytes(dtype, M, F), workspace, ws_bytes, &ws);
+  st = take_workspace(dev, need, workspace, ws_bytes, &ws);
   if (st != GEMM_OK) return st;
-  return dtype == GEMM_DT_F32
-             ? run_backward<float>(act, op_w, M, D, F, dH, lddh, X, ldx, Wg, ldwg, Wu, ldwu, G,
-                                   ldg, U, ldu, dX, lddx, dWg, lddwg, dWu, lddwu, ws, stream)
-             : run_backward<bf16>(act, op_w, M, D, F, dH, lddh, X, ldx, Wg, ldwg, Wu, ldwu, G, ldg,
-                                  U, ldu, dX, lddx, dWg, lddwg, dWu, lddwu, ws, stream);
+  uint8_t *at = static_cast<uint8_t *>(ws);
+  Layout lay{dtype, at + 2 * part};
+  bf16 *dg = reinterpret_cast<bf16 *>(at), *du = reinterpret_cast<bf16 *>(at + part);
+  const int64_t ld = round8(F);
+  const DgateArgs gate{M, F, act, dH, lddh, G, U, ldg, ldu, dg, du, ld, M * ld};
+  // dG and dU as an operand whose summed index is the width F (dX) or the token (dW)
+  auto grad = [&](const bf16 *p, int mn_major) {
+    return FfOperand{p, F, M, ld, M * ld, mn_major};
+  };
+  FfProduct px{}, pw{};
+  px.planes = pw.planes = planes_of(dtype);
+  if (dX) {
+    px.kind = kFfConcat;
+    px.M = M;
+    px.N = D;
+    px.K = F;
+    px.a[0] = grad(dg, 0);
+    px.a[1] = grad(du, 0);
+    px.b[0] = lay.operand(wg, op_w == GEMM_OP_T);
+    px.b[1] = lay.operand(wu, op_w == GEMM_OP_T);
+    px.c[0] = dX;
+    px.ldc = lddx;
+  }
+  if (dWg) {
+    // stored D x F: X^T dG; stored F x D: dG^T X
+    const FfOperand ox = lay.operand(x, 1);
+    pw.kind = kFfBatch;
+    pw.M = wr;
+    pw.N = wc;
+    pw.K = M;
+    pw.a[0] = op_w == GEMM_OP_N ? ox : grad(dg, 1);
+    pw.b[0] = op_w == GEMM_OP_N ? grad(dg, 1) : ox;
+    pw.a_two = op_w == GEMM_OP_T;
+    pw.b_two = op_w == GEMM_OP_N;
+    (op_w == GEMM_OP_N ? pw.b : pw.a)[1] = grad(du, 1);
+    pw.c[0] = dWg;
+    pw.c[1] = dWu;
+    pw.ldc = lddwg;
+    pw.ldc2 = lddwu;
+  }
+  cudaError_t e = launch_pack(lay.jobs, lay.n, dtype, dp.sm_count, stream);
+  if (e == cudaSuccess) e = launch_dgate(gate, dtype, dp.sm_count, stream);
+  if (e != cudaSuccess) return to_status(e);
+  if (dX) st = launch_ff_product(px, dp, stream);
+  if (st == GEMM_OK && dWg) st = launch_ff_product(pw, dp, stream);
+  return st;
 }

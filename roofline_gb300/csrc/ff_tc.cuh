@@ -1,0 +1,65 @@
+// The tensor-core products of the gated feed-forward block (ff_tc.cu) and the
+// passes that lay their operands out (ff_pack.cu).
+#pragma once
+
+#include "ff.cuh"
+
+namespace gg {
+
+// A BF16 operand of one product: `planes` matrices of `outer` rows of `inner`
+// contiguous elements, rows `ld` and planes `plane` elements apart.  A FP32
+// matrix x is three planes x0 + x1 + x2, each the BF16 nearest to what the
+// ones before it leave: 24 bits.  mn_major = 0: inner is the summed extent K
+// and the rows are rows of A or columns of B; 1: the other way round.
+struct FfOperand {
+  const bf16 *p;
+  int64_t inner, outer, ld, plane;
+  int mn_major;
+};
+
+// Products of M x K and K x N operands, BF16 planes in, FP32 sums:
+//   gated:  c0 = act(a0 b0) * (a0 b1), with the sums to g and u if given
+//   concat: c0 = a0 b0 + a1 b1
+//   batch:  c0 = a0 b0, c1 = a[a_two] b[b_two]
+// Outputs are BF16 for one plane and FP32 for three.
+enum FfKind { kFfGated, kFfConcat, kFfBatch };
+struct FfProduct {
+  FfKind kind;
+  int planes, act;
+  int64_t M, N, K;
+  FfOperand a[2], b[2];
+  int a_two, b_two;  // batch: which operands the second product takes
+  void *c[2];
+  int64_t ldc, ldc2;  // of c0 and c1
+  float *g, *u;
+  int64_t ldg, ldu;
+};
+// Enqueues it; returns a GEMM_* status.
+int launch_ff_product(const FfProduct &p, const DeviceProps &dp, cudaStream_t s);
+int ff_read_and_clear_status();
+
+// Lays one matrix (rows x cols, row stride ld, FP32 or BF16) out as BF16
+// planes whose rows TMA can read: ld_out a multiple of 8, 16-byte aligned.
+struct PackJob {
+  const void *src;
+  int64_t rows, cols, ld;
+  bf16 *dst;
+  int64_t ld_out, plane;
+};
+constexpr int kPackJobs = 3;
+cudaError_t launch_pack(const PackJob *jobs, int n, int dtype, int sms, cudaStream_t s);
+
+// dG = dH * U * act'(G) and dU = dH * act(G), M x F, as such planes.
+struct DgateArgs {
+  int64_t M, F;
+  int act;
+  const void *dh;
+  int64_t lddh;
+  const float *g, *u;
+  int64_t ldg, ldu;
+  bf16 *dg, *du;
+  int64_t ld_out, plane;
+};
+cudaError_t launch_dgate(const DgateArgs &p, int dtype, int sms, cudaStream_t s);
+
+}  // namespace gg

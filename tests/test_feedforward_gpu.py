@@ -71,6 +71,16 @@ def test_forward_and_backward(ff, size, dt, order):
     _check_backward(ff, dH, X, Wg, Wu, G, U, act)
 
 
+@pytest.mark.parametrize("order", ["oi", "io"])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1100, 200, 2100), (2500, 2200, 264), (264, 2200, 2500)])
+def test_products_that_fill_the_gpu(ff, size, dt, order):
+    """Enough tiles for pairs of CTAs: the forward product, dX and dW in turn."""
+    X, Wg, Wu, dH = _case(sum(size), *size, dt, order)
+    G, U = _check_forward(ff, X, Wg, Wu, "silu")
+    _check_backward(ff, dH, X, Wg, Wu, G, U, "silu")
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_activations(ff, dt, act):
