@@ -4,6 +4,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace gg {
@@ -31,26 +33,26 @@ __device__ __forceinline__ float sigmoid(float x) {
   return FAST ? __fdividef(1.0f, 1.0f + __expf(-x)) : 1.0f / (1.0f + expf(-x));
 }
 
-template <bool FAST>
-__device__ __forceinline__ float act_value(float g, int act) {
-  if (act == GEMM_ACT_SILU) return g * sigmoid<FAST>(g);
-  if (act == GEMM_ACT_RELU) return g > 0.0f ? g : (g != g ? g : 0.0f);
-  if (act == GEMM_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678f));
+template <bool FAST, int ACT>
+__device__ __forceinline__ float act_of(float g) {
+  if (ACT == GEMM_ACT_SILU) return g * sigmoid<FAST>(g);
+  if (ACT == GEMM_ACT_RELU) return g > 0.0f ? g : (g != g ? g : 0.0f);
+  if (ACT == GEMM_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678f));
   // (1 + tanh(u)) / 2 = sigmoid(2u)
   return g * sigmoid<FAST>(2.0f * 0.79788456f * (g + 0.044715f * g * g * g));
 }
 
 // act(g) and act'(g).
-template <bool FAST>
-__device__ __forceinline__ void act_both(float g, int act, float &a, float &d) {
-  if (act == GEMM_ACT_SILU) {
+template <bool FAST, int ACT>
+__device__ __forceinline__ void act_both(float g, float &a, float &d) {
+  if (ACT == GEMM_ACT_SILU) {
     const float s = sigmoid<FAST>(g);
     a = g * s;
     d = s * (1.0f + g * (1.0f - s));
-  } else if (act == GEMM_ACT_RELU) {
-    a = g > 0.0f ? g : (g != g ? g : 0.0f);
+  } else if (ACT == GEMM_ACT_RELU) {
+    a = act_of<FAST, ACT>(g);
     d = g > 0.0f ? 1.0f : 0.0f;
-  } else if (act == GEMM_ACT_GELU) {
+  } else if (ACT == GEMM_ACT_GELU) {
     const float p = 0.5f * (1.0f + erff(g * 0.70710678f));
     a = g * p;
     d = p + g * 0.39894228f * (FAST ? __expf(-0.5f * g * g) : expf(-0.5f * g * g));
@@ -58,6 +60,19 @@ __device__ __forceinline__ void act_both(float g, int act, float &a, float &d) {
     const float s = sigmoid<FAST>(2.0f * 0.79788456f * (g + 0.044715f * g * g * g));
     a = g * s;
     d = s + 2.0f * g * s * (1.0f - s) * 0.79788456f * (1.0f + 0.134145f * g * g);
+  }
+}
+
+// f with the activation as a compile-time value: the choice is made once for
+// a block of values, not for each (unrolled 32 times, the four branches were
+// more code than the instruction cache holds).
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case GEMM_ACT_SILU: f(std::integral_constant<int, GEMM_ACT_SILU>()); break;
+    case GEMM_ACT_GELU: f(std::integral_constant<int, GEMM_ACT_GELU>()); break;
+    case GEMM_ACT_GELU_TANH: f(std::integral_constant<int, GEMM_ACT_GELU_TANH>()); break;
+    default: f(std::integral_constant<int, GEMM_ACT_RELU>()); break;
   }
 }
 

@@ -1,6 +1,7 @@
 // Passes around the feed-forward products: operands that TMA cannot read (or
 // FP32 ones) laid out as BF16 planes, and the gradients of the gate.
 #include "ff_tc.cuh"
+#include "tc_common.cuh"
 
 namespace gg {
 namespace {
@@ -70,7 +71,9 @@ struct PackJobs {
 };
 
 template <typename T, int P>
-__global__ void __launch_bounds__(256) ff_pack_kernel(const PackJobs jobs) {
+__global__ void __launch_bounds__(256) ff_pack_kernel(PackJobs jobs) {
+  tc::grid_dependency_wait();
+  tc::grid_launch_dependents();
   for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < jobs.first[jobs.n];
        e += gridDim.x * 256ll) {
     int k = 0;
@@ -86,7 +89,9 @@ __global__ void __launch_bounds__(256) ff_pack_kernel(const PackJobs jobs) {
 }
 
 template <typename T, int P>
-__global__ void __launch_bounds__(256) ff_dgate_kernel(const DgateArgs p) {
+__global__ void __launch_bounds__(256) ff_dgate_kernel(DgateArgs p) {
+  tc::grid_dependency_wait();
+  tc::grid_launch_dependents();
   const int64_t per_row = p.ld_out / 8, n = p.M * per_row;
   const T *dh = static_cast<const T *>(p.dh);
   const bool vh = rows_aligned(dh, p.lddh), vg = rows_aligned(p.g, p.ldg),
@@ -97,15 +102,34 @@ __global__ void __launch_bounds__(256) ff_dgate_kernel(const DgateArgs p) {
     load8(dh + r * p.lddh, c, p.F, vh, h);
     load8(p.g + r * p.ldg, c, p.F, vg, g);
     load8(p.u + r * p.ldu, c, p.F, vu, u);
+    with_act(p.act, [&](auto act) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) act_both<P == 1, decltype(act)::value>(g[i], a[i], d[i]);
+    });
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      act_both<P == 1>(g[i], p.act, a[i], d[i]);
       d[i] = h[i] * u[i] * d[i];
       a[i] = h[i] * a[i];
     }
     store8<P>(d, p.dg + r * p.ld_out + c, p.plane);
     store8<P>(a, p.du + r * p.ld_out + c, p.plane);
   }
+}
+
+// Launched with programmatic dependent launch: scheduled while the kernel
+// before it drains, for which every thread of it waits first.
+template <typename Args>
+cudaError_t launch(void (*kern)(Args), int grid, const Args &p, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)grid);
+  lc.blockDim = dim3(256);
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kern, p);
 }
 
 int blocks_for(int64_t groups, int sms) {
@@ -126,20 +150,16 @@ cudaError_t launch_pack(const PackJob *jobs, int n, int dtype, int sms, cudaStre
   if (p.n == 0) return cudaSuccess;
   const int grid = blocks_for(p.first[p.n], sms);
   if (dtype == GEMM_DT_F32)
-    ff_pack_kernel<float, 3><<<grid, 256, 0, s>>>(p);
-  else
-    ff_pack_kernel<bf16, 1><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+    return launch(ff_pack_kernel<float, 3>, grid, p, s);
+  return launch(ff_pack_kernel<bf16, 1>, grid, p, s);
 }
 
 cudaError_t launch_dgate(const DgateArgs &p, int dtype, int sms, cudaStream_t s) {
   if (p.M == 0 || p.F == 0) return cudaSuccess;
   const int grid = blocks_for(p.M * (p.ld_out / 8), sms);
   if (dtype == GEMM_DT_F32)
-    ff_dgate_kernel<float, 3><<<grid, 256, 0, s>>>(p);
-  else
-    ff_dgate_kernel<bf16, 1><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+    return launch(ff_dgate_kernel<float, 3>, grid, p, s);
+  return launch(ff_dgate_kernel<bf16, 1>, grid, p, s);
 }
 
 }  // namespace gg

@@ -33,7 +33,7 @@ __device__ int g_ff_status;  // 0 = ok, else a GEMM_ERR_* code
 // warp 0: TMA, warp 1: MMA, warps 2..9: epilogue, two for each 32 rows
 constexpr int kThreadsFF = 320;
 constexpr int kEpiWarps = 8;
-constexpr int kFlush = 2;
+constexpr int kFlush = 4;
 
 struct FfParams {
   int64_t M, N;        // output extents (of one matrix)
@@ -41,6 +41,9 @@ struct FfParams {
   int tiles_m, tiles_n, batches, group_n;
   int a_seg, a_batch, b_seg, b_batch;  // operand = segment * x_seg + batch * x_batch
   int a_mn, b_mn;      // operands stored MN-major
+  int bn, out_cols;    // a tile's accumulator and output columns
+  int a_bytes, b_bytes;  // one plane of a stage: A's rows and B's columns in this CTA
+  int stages;
   int act;
   void *c[2];
   int64_t ldc[2];
@@ -50,31 +53,15 @@ struct FfParams {
   int stall_producer;  // test hook: the producer issues nothing
 };
 
-// CG: CTAs that share one tile of CG * 128 rows (a pair splits the columns of
-// B between its two shared memories).  BN: accumulator columns of a tile; the
-// gated form gives half of them to each of its two sums.  P: planes.
-template <int P, int CG, int BN, bool GATED>
-struct FfCfg {
-  static constexpr int BK = 64;                     // 128 bytes of K, one swizzle line
-  static constexpr int B_ROWS = BN / CG;            // columns of B in this CTA
-  static constexpr int A_BYTES = 128 * BK * 2;      // one plane
-  static constexpr int B_BYTES = B_ROWS * BK * 2;
-  static constexpr int STAGE_BYTES = P * (A_BYTES + B_BYTES);
-  static constexpr int EPI_BYTES = kEpiWarps * 32 * 128;  // 32 rows x 128 bytes per warp
-  static constexpr int BUDGET = 227 * 1024 - 1024 - 256 - EPI_BYTES;
-  static constexpr int FIT = BUDGET / STAGE_BYTES;
-  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256 + EPI_BYTES;
-  // two accumulators: one plane, one is filled while the other is drained;
-  // three planes, the large and the small products
-  static constexpr int ACCS = 2;
-  static constexpr int TMEM_COLS = ACCS * BN;
-  static constexpr int OUT_COLS = GATED ? BN / 2 : BN;
-  // columns of B one load brings: the gated form takes each half of a single
-  // CTA's columns, or all of one CTA of a pair, from one of the two matrices
-  static constexpr int B_LOAD = GATED && CG == 1 ? BN / 2 : B_ROWS;
-  static_assert(TMEM_COLS <= 512 && STAGES >= 2, "");
-};
+constexpr int kLine = 128;       // bytes of one row of a stage: 64 of K, a swizzle line
+constexpr int kBlockK = 64;
+constexpr int kMaxStages = 12;
+constexpr int kEpiBytes = kEpiWarps * 4096;  // 32 x 16 values, twice, per warp
+constexpr int kStageBudget = 227 * 1024 - 1024 - 256 - kEpiBytes;
+constexpr int kTmemCols = 512;   // two accumulators of at most 256 columns:
+// one plane, one is filled while the other is drained; three planes, the
+// large and the small products
+constexpr int kAccCols = 256;
 
 // Waits for the phase of `bar` with the given parity, at most ns; gives up at
 // once when another role of the CTA has.
@@ -225,45 +212,122 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
       : "r"(taddr));
 }
 
-// Stores a warp's 32 x 32 block: lane r holds row r.  dst is row 0, column 0
-// of it, rows and cols what lies inside the matrix.  The block goes through
-// the warp's shared memory in 16-byte pieces, swizzled so that neither side
-// has bank conflicts, and leaves as whole rows of 64 (BF16) or 128 bytes; a
-// clipped or unaligned block leaves element by element.
-template <typename T>
-__device__ __forceinline__ void store_block(uint8_t *st, const float (&v)[32], T *dst, int64_t ld,
-                                            int rows, int cols, bool vec) {
-  constexpr int PER = 16 / sizeof(T);      // values of a piece
-  constexpr int PIECES = 32 / PER;         // pieces of a row: 4 or 8
-  constexpr int ROW = 32 * sizeof(T);
-  const int lane = threadIdx.x & 31;
-  auto at = [](int r, int k) {
-    return r * ROW + ((k ^ (PIECES == 8 ? r & 7 : (r >> 1) & 3)) * 16);
-  };
-#pragma unroll
-  for (int k = 0; k < PIECES; ++k) {
-    __align__(16) T t[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) t[i] = from_f32<T>(v[k * PER + i]);
-    *reinterpret_cast<uint4 *>(st + at(lane, k)) = *reinterpret_cast<const uint4 *>(t);
+// What a warp's blocks of 32 rows x 16 columns become: c = v, or (gated)
+// act(v) * w with v and w themselves to g and u if given.
+template <typename T, bool GATED, bool FAST>
+struct Writer {
+  uint8_t *st;  // the warp's 4 KB of shared memory: v, then w
+  T *c;
+  float *g, *u;  // row 0 of the warp's rows, column 0 of the matrix
+  int64_t ldc, ldg, ldu, N;
+  int rows, act;
+  bool vec_c, vec_gu;  // every row of c, of g and u, starts on a 16-byte boundary
+
+  // Row r's 16-byte piece k: swizzled so that a quarter warp that writes one
+  // piece of 8 rows, or reads the 4 of 2 rows, meets each bank once.
+  __device__ __forceinline__ static int piece(int r, int k) {
+    return r * 64 + ((k ^ ((r >> 1) & 3)) * 16);
   }
-  __syncwarp();
-  if (vec && cols >= 32) {
+
+  // act(x) * y for eight values at once: one choice of the activation, and
+  // eight chains of arithmetic in flight in a warp that has few neighbours.
+  __device__ __forceinline__ void combine(float (&x)[8], const float (&y)[8]) const {
+    with_act(act, [&](auto a) {
 #pragma unroll
-    for (int it = 0; it < PIECES; ++it) {
-      const int r = it * (32 / PIECES) + lane / PIECES, k = lane % PIECES;
-      if (r < rows)
-        *reinterpret_cast<uint4 *>(dst + r * ld + k * PER) =
-            *reinterpret_cast<const uint4 *>(st + at(r, k));
+      for (int i = 0; i < 8; ++i) x[i] = act_of<FAST, decltype(a)::value>(x[i]) * y[i];
+    });
+  }
+
+  // Columns [col, col + 16): lane r holds row r.  The values go through shared
+  // memory and are finished where they leave: four of a row to a lane, or one
+  // of a row in a clipped or unaligned block, so that rows leave in whole
+  // sectors.
+  __device__ __forceinline__ void block(int64_t col, const float *v, const float *w) const {
+    const int lane = threadIdx.x & 31;
+    if (rows <= 0 || col >= N) return;
+    const int cols = N - col < 16 ? (int)(N - col) : 16;
+    const uint8_t *sw = st + 2048;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      *reinterpret_cast<float4 *>(st + piece(lane, k)) =
+          make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      if (GATED)
+        *reinterpret_cast<float4 *>(st + 2048 + piece(lane, k)) =
+            make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     }
-  } else if (lane < cols) {
+    __syncwarp();
+    if (GATED && g) {
+      if (vec_gu && cols == 16) {
+        const int k = lane & 3;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const int r = it * 8 + (lane >> 2);
+          if (r >= rows) continue;
+          *reinterpret_cast<float4 *>(g + r * ldg + col + 4 * k) =
+              *reinterpret_cast<const float4 *>(st + piece(r, k));
+          *reinterpret_cast<float4 *>(u + r * ldu + col + 4 * k) =
+              *reinterpret_cast<const float4 *>(sw + piece(r, k));
+        }
+      } else {
+        const int j = lane & 15, off = (j & 3) * 4;
 #pragma unroll 4
-    for (int r = 0; r < rows; ++r)
-      dst[r * ld + lane] =
-          *reinterpret_cast<const T *>(st + at(r, lane / PER) + (lane % PER) * sizeof(T));
+        for (int r = lane >> 4; r < 32; r += 2) {
+          if (j >= cols || r >= rows) continue;
+          g[r * ldg + col + j] = *reinterpret_cast<const float *>(st + piece(r, j >> 2) + off);
+          u[r * ldu + col + j] = *reinterpret_cast<const float *>(sw + piece(r, j >> 2) + off);
+        }
+      }
+    }
+    float x[8], y[8];
+    if (!c) {
+    } else if (vec_c && cols == 16) {
+      const int k = lane & 3;
+      const int64_t at = col + 4 * k;
+#pragma unroll 1
+      for (int r0 = lane >> 2; r0 < 32; r0 += 16) {  // rows r0 and r0 + 8
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 f = *reinterpret_cast<const float4 *>(st + piece(r0 + 8 * h, k));
+          x[4 * h] = f.x, x[4 * h + 1] = f.y, x[4 * h + 2] = f.z, x[4 * h + 3] = f.w;
+          if (GATED) {
+            const float4 e = *reinterpret_cast<const float4 *>(sw + piece(r0 + 8 * h, k));
+            y[4 * h] = e.x, y[4 * h + 1] = e.y, y[4 * h + 2] = e.z, y[4 * h + 3] = e.w;
+          }
+        }
+        if (GATED) combine(x, y);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = r0 + 8 * h;
+          __align__(16) T t[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = from_f32<T>(x[4 * h + i]);
+          if (r < rows) {
+            if constexpr (sizeof(T) == 4)
+              *reinterpret_cast<float4 *>(c + r * ldc + at) = *reinterpret_cast<float4 *>(t);
+            else
+              *reinterpret_cast<uint2 *>(c + r * ldc + at) = *reinterpret_cast<uint2 *>(t);
+          }
+        }
+      }
+    } else {
+      const int j = lane & 15, off = (j & 3) * 4, last = j < cols ? rows : 0;
+#pragma unroll 1
+      for (int r0 = lane >> 4; r0 < 32; r0 += 16) {  // rows r0, r0 + 2, ..., r0 + 14
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          x[h] = *reinterpret_cast<const float *>(st + piece(r0 + 2 * h, j >> 2) + off);
+          if (GATED)
+            y[h] = *reinterpret_cast<const float *>(sw + piece(r0 + 2 * h, j >> 2) + off);
+        }
+        if (GATED) combine(x, y);
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+          if (r0 + 2 * h < last) c[(r0 + 2 * h) * ldc + col + j] = from_f32<T>(x[h]);
+      }
+    }
+    __syncwarp();  // the block's place is written again
   }
-  __syncwarp();
-}
+};
 
 struct TileAt {
   int64_t m, n;
@@ -282,22 +346,28 @@ __device__ __forceinline__ TileAt tile_at(const FfParams &p, int64_t t) {
   return {local / width, first + local % width, batch};
 }
 
+// CG: CTAs that share one tile of CG * 128 rows (a pair splits the columns of
+// B between its two shared memories).  BN: accumulator columns of a tile, of
+// which the gated form gives half to each of its two sums; with one plane it
+// is chosen at run time (BN = 0).  P: planes.
 template <int P, int CG, int BN, bool GATED>
 __global__ void __launch_bounds__(kThreadsFF, 1)
 ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CUtensorMap ma1,
              const __grid_constant__ CUtensorMap mb0, const __grid_constant__ CUtensorMap mb1,
              const FfParams p) {
-  using Cfg = FfCfg<P, CG, BN, GATED>;
+  static_assert((P == 1) == (BN == 0), "");
   using T = typename std::conditional<P == 1, bf16, float>::type;
-  constexpr int STAGES = Cfg::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + STAGES * Cfg::STAGE_BYTES);
-  uint64_t *empty = full + STAGES;
-  uint64_t *acc_full = empty + STAGES;      // [ACCS]
-  uint64_t *acc_empty = acc_full + Cfg::ACCS;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + Cfg::ACCS);
+  const int bn = P == 1 ? p.bn : BN;
+  const uint32_t stages = (uint32_t)p.stages;
+  const uint32_t stage_bytes = P * (uint32_t)(p.a_bytes + p.b_bytes);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + stages * stage_bytes);
+  uint64_t *empty = full + kMaxStages;
+  uint64_t *acc_full = empty + kMaxStages;  // [2]
+  uint64_t *acc_empty = acc_full + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   uint8_t *epi = reinterpret_cast<uint8_t *>(full) + 256;
 
@@ -308,78 +378,92 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
   const int kbs = p.kb * p.segs;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (uint32_t s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int i = 0; i < Cfg::ACCS; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], CG * kEpiWarps);  // every epilogue warp of the tile
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) ff_tmem_alloc<CG>(tmem_slot, Cfg::TMEM_COLS);
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&ma0);
+    prefetch_tmap(&mb0);
+    if (p.segs > 1 || p.batches > 1 || GATED) {
+      prefetch_tmap(&ma1);
+      prefetch_tmap(&mb1);
+    }
+  }
+  if (warp == 1) ff_tmem_alloc<CG>(tmem_slot, kTmemCols);
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // operands come from the passes before it in the stream
+  grid_dependency_wait();
+  grid_launch_dependents();
 
   bool ok = true;
   if (warp == 0) {
     // ---------------- producer: this CTA's rows of A and columns of B
-    uint32_t issued = 0;
     if (lane == 0 && !p.stall_producer) {
+      uint32_t s = 0, ph = 1, issued = 0;
+      auto take = [&] {
+        ok = ff_wait(&empty[s], ph, p.wait_ns, abort_flag);
+        return ok;
+      };
+      auto next = [&] {
+        if (++s == stages) s = 0, ph ^= 1;
+      };
+      const int b_rows = p.b_bytes / kLine;
       for (int64_t t = worker; ok && t < tiles; t += workers) {
         const TileAt at = tile_at(p, t);
         const int32_t m0 = (int32_t)(at.m * (CG * 128) + rank * 128);
-        const int32_t n0 = (int32_t)(at.n * Cfg::OUT_COLS);
-        for (int kb = 0; kb < kbs; ++kb, ++issued) {
-          const uint32_t s = issued % STAGES;
-          if (!ff_wait(&empty[s], ((issued / STAGES) & 1u) ^ 1u, p.wait_ns,
-                       abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_expect_tx(&full[s], CG * Cfg::STAGE_BYTES);
+        const int32_t n0 = (int32_t)(at.n * p.out_cols);
+        for (int kb = 0; kb < kbs && take(); ++kb, ++issued, next()) {
+          if (rank == 0) mbar_expect_tx(&full[s], CG * stage_bytes);
           const uint32_t bar =
               CG == 1 ? smem_u32(&full[s]) : map_to_cta(smem_u32(&full[s]), 0);
           const int seg = kb >= p.kb;
-          const int32_t k0 = (kb - seg * p.kb) * Cfg::BK;
+          const int32_t k0 = (kb - seg * p.kb) * kBlockK;
           const CUtensorMap *ma = seg * p.a_seg + at.batch * p.a_batch ? &ma1 : &ma0;
           const CUtensorMap *mb = seg * p.b_seg + at.batch * p.b_batch ? &mb1 : &mb0;
-          const uint32_t a = smem_u32(smem + s * Cfg::STAGE_BYTES), b = a + P * Cfg::A_BYTES;
+          const uint32_t a = smem_u32(smem) + s * stage_bytes, b = a + P * (uint32_t)p.a_bytes;
 #pragma unroll
           for (int q = 0; q < P; ++q) {
-            load_tile<CG>(a + q * Cfg::A_BYTES, ma, bar, p.a_mn, 128, m0, k0, q);
-            const uint32_t bq = b + q * Cfg::B_BYTES;
+            load_tile<CG>(a + q * p.a_bytes, ma, bar, p.a_mn, 128, m0, k0, q);
+            const uint32_t bq = b + q * p.b_bytes;
             if constexpr (!GATED) {
-              load_tile<CG>(bq, mb, bar, p.b_mn, Cfg::B_ROWS, n0 + (int)rank * Cfg::B_ROWS, k0, q);
+              load_tile<CG>(bq, mb, bar, p.b_mn, b_rows, n0 + (int)rank * b_rows, k0, q);
             } else if constexpr (CG == 2) {
-              load_tile<CG>(bq, rank ? &mb1 : &mb0, bar, p.b_mn, Cfg::B_ROWS, n0, k0, q);
+              load_tile<CG>(bq, rank ? &mb1 : &mb0, bar, p.b_mn, b_rows, n0, k0, q);
             } else {
-              load_tile<CG>(bq, &mb0, bar, p.b_mn, BN / 2, n0, k0, q);
-              load_tile<CG>(bq + BN / 2 * 128, &mb1, bar, p.b_mn, BN / 2, n0, k0, q);
+              load_tile<CG>(bq, &mb0, bar, p.b_mn, b_rows / 2, n0, k0, q);
+              load_tile<CG>(bq + p.b_bytes / 2, &mb1, bar, p.b_mn, b_rows / 2, n0, k0, q);
             }
           }
         }
       }
       // Every stage handed back: no load is in flight and no arrival from the
       // pair's MMAs still on its way here.
-      for (uint32_t it = issued > STAGES ? issued - STAGES : 0; ok && it < issued; ++it)
-        if (!ff_wait(&empty[it % STAGES], (it / STAGES) & 1u, p.wait_ns, abort_flag))
-          ok = false;
+      for (uint32_t i = 0; i < stages && i < issued && ok; ++i) {
+        take();
+        next();
+      }
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (of the pair)
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.a_mn << 15) |
-                             ((uint32_t)p.b_mn << 16) | ((uint32_t)(BN >> 3) << 17) |
+                             ((uint32_t)p.b_mn << 16) | ((uint32_t)(bn >> 3) << 17) |
                              ((uint32_t)((CG * 128) >> 4) << 24);
       // 16 along K: 32 bytes of a K-major line, two 8-deep groups MN-major
       const uint64_t astep = p.a_mn ? 2048 >> 4 : 32 >> 4, bstep = p.b_mn ? 2048 >> 4 : 32 >> 4;
-      uint32_t it = 0, used[2] = {0, 0};  // K blocks; times each accumulator was filled
+      uint32_t s = 0, ph = 0, used[2] = {0, 0};  // stage; times each accumulator was filled
       // Before accumulator i is filled anew, the epilogue has read it.
       auto take = [&](int i) {
         ok = ff_wait(&acc_empty[i], (used[i]++ & 1u) ^ 1u, p.wait_ns, abort_flag);
@@ -390,54 +474,58 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
       for (int64_t t = worker; ok && t < tiles; t += workers, ++done) {
         const int acc = P == 1 ? done & 1 : 0;
         if (P == 1 && !take(acc)) break;
-        const uint32_t d = tmem_base + (uint32_t)(acc * BN);
-        for (int kb = 0; kb < kbs; ++kb, ++it) {
-          const uint32_t s = it % STAGES;
-          if (!ff_wait(&full[s], (it / STAGES) & 1u, p.wait_ns, abort_flag)) {
+        const uint32_t d = tmem_base + (uint32_t)(acc * kAccCols);
+        for (int kb = 0; kb < kbs; ++kb) {
+          if (!ff_wait(&full[s], ph, p.wait_ns, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + s * Cfg::STAGE_BYTES), b = a + P * Cfg::A_BYTES;
+          const uint32_t a = smem_u32(smem) + s * stage_bytes, b = a + P * (uint32_t)p.a_bytes;
           const uint64_t da = tile_desc(a, p.a_mn), db = tile_desc(b, p.b_mn);
           if (P == 3 && kb % kFlush == 0 && !take(0)) break;
           const bool first = P == 1 ? kb == 0 : kb % kFlush == 0;
 #pragma unroll
-          for (int kk = 0; kk < Cfg::BK / 16; ++kk)
+          for (int kk = 0; kk < kBlockK / 16; ++kk)
             mma_bf16<CG>(d, da + kk * astep, db + kk * bstep, idesc, first && kk == 0 ? 0u : 1u);
           if constexpr (P == 3) {
             if (kb % kFlush == kFlush - 1 || kb == kbs - 1) commit<CG>(&acc_full[0]);
             if (kb == 0 && !take(1)) break;
 #pragma unroll
-            for (int kk = 0; kk < Cfg::BK / 16; ++kk) {
+            for (int kk = 0; kk < kBlockK / 16; ++kk) {
 #pragma unroll
               for (int sum = P - 1; sum >= 1; --sum) {
 #pragma unroll
                 for (int i = 0; i <= sum; ++i)
-                  mma_bf16<CG>(d + BN, da + kk * astep + (uint64_t)(i * (Cfg::A_BYTES >> 4)),
-                               db + kk * bstep + (uint64_t)((sum - i) * (Cfg::B_BYTES >> 4)),
+                  mma_bf16<CG>(d + kAccCols, da + kk * astep + (uint64_t)(i * (p.a_bytes >> 4)),
+                               db + kk * bstep + (uint64_t)((sum - i) * (p.b_bytes >> 4)),
                                idesc, (kb > 0 || kk > 0 || sum < P - 1 || i > 0) ? 1u : 0u);
               }
             }
           }
           commit<CG>(&empty[s]);
+          if (++s == stages) s = 0, ph ^= 1;
         }
         if (ok) commit<CG>(&acc_full[P == 1 ? acc : 1]);
       }
     }
   } else {
     // ---------------- epilogue: a warp has 32 rows (the tensor-memory lanes
-    // 32 (w & 3) on) and half the columns of the tile
+    // 32 (w & 3) on) and every second 16 columns of the tile
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    constexpr int COLS = Cfg::OUT_COLS / 2;
-    uint8_t *st = epi + (warp - 2) * (32 * 128);
+    uint8_t *st = epi + (warp - 2) * 4096;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
     auto aligned = [](const void *q, int64_t ld, int64_t size) {
       return ((reinterpret_cast<uintptr_t>(q) | (uintptr_t)(ld * size)) & 15) == 0;
     };
-    const bool vec_c = aligned(p.c[0], p.ldc[0], sizeof(T)) &&
-                       aligned(p.c[1], p.ldc[1], sizeof(T));
-    const bool vec_g = aligned(p.g, p.ldg, 4), vec_u = aligned(p.u, p.ldu, 4);
+    Writer<T, GATED, P == 1> out;
+    out.st = st;
+    out.N = p.N;
+    out.act = p.act;
+    out.ldg = p.ldg;
+    out.ldu = p.ldu;
+    out.vec_c = aligned(p.c[0], p.ldc[0], sizeof(T)) && aligned(p.c[1], p.ldc[1], sizeof(T));
+    out.vec_gu = aligned(p.g, p.ldg, 4) && aligned(p.u, p.ldu, 4);
     uint32_t used[2] = {0, 0};
     // tcgen05.ld is warp-collective: the warp proceeds or stops as one
     auto wait_full = [&](int i) {
@@ -454,70 +542,54 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
     for (int64_t t = worker; ok && t < tiles; t += workers, ++done) {
       const TileAt at = tile_at(p, t);
       const int64_t r0 = at.m * (CG * 128) + rank * 128 + quarter * 32;
-      const int64_t c0 = at.n * Cfg::OUT_COLS + half * COLS;
-      const int rows = (int)(p.M - r0 < 32 ? (p.M - r0 > 0 ? p.M - r0 : 0) : 32);
-      T *c = static_cast<T *>(p.c[at.batch]);
-      const int64_t ldc = p.ldc[at.batch];
-      // 32 columns from c0 + j on: v the sums (of the gate), w those of b1
-      auto finish = [&](int j, float (&v)[32], const float (&w)[32]) {
-        const int64_t left = p.N - c0 - j;
-        if (left <= 0 || rows == 0) return;
-        const int cols = left < 32 ? (int)left : 32;
-        if constexpr (GATED) {
-          if (p.g) {
-            store_block<float>(st, v, p.g + r0 * p.ldg + c0 + j, p.ldg, rows, cols, vec_g);
-            store_block<float>(st, w, p.u + r0 * p.ldu + c0 + j, p.ldu, rows, cols, vec_u);
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = act_value<P == 1>(v[i], p.act) * w[i];
-        }
-        if (c) store_block<T>(st, v, c + r0 * ldc + c0 + j, ldc, rows, cols, vec_c);
-      };
+      const int64_t c0 = at.n * p.out_cols;
+      out.rows = (int)(p.M - r0 < 32 ? p.M - r0 : 32);
+      out.ldc = p.ldc[at.batch];
+      out.c = static_cast<T *>(p.c[at.batch]);
+      if (out.c) out.c += r0 * out.ldc;
+      out.g = p.g ? p.g + r0 * p.ldg : nullptr;
+      out.u = p.u ? p.u + r0 * p.ldu : nullptr;
       if constexpr (P == 1) {
         const int acc = done & 1;
         if (!wait_full(acc)) break;
-        const uint32_t base = lane_base + (uint32_t)(acc * BN + half * COLS);
+        const uint32_t base = lane_base + (uint32_t)(acc * kAccCols);
+        int j = 16 * half;
+        if (j >= p.out_cols) release(acc);
 #pragma unroll 1
-        for (int j = 0; j < COLS; j += 32) {
-          float v[32], w[32];
-          tmem_ld32(base + (uint32_t)j, reinterpret_cast<uint32_t(&)[32]>(v));
-          if constexpr (GATED)
-            tmem_ld32(base + (uint32_t)(BN / 2 + j), reinterpret_cast<uint32_t(&)[32]>(w));
+        for (; j < p.out_cols; j += 32) {
+          float v[16], w[16];
+          tmem_ld16(base + (uint32_t)j, v);
+          if constexpr (GATED) tmem_ld16(base + (uint32_t)(p.out_cols + j), w);
           tmem_ld_wait();
-          if (j + 32 >= COLS) release(acc);
-          finish(j, v, w);
+          if (j + 32 >= p.out_cols) release(acc);
+          out.block(c0 + j, v, w);
         }
       } else {
-        constexpr int BLOCKS = (GATED ? 2 : 1) * COLS / 32;
-        float sum[BLOCKS][32];
+        constexpr int COLS = GATED ? BN / 4 : BN / 2;  // output columns of a warp
+        constexpr int BLOCKS = BN / 32;                // 16 columns of the sums each
+        float sum[BLOCKS][16];
 #pragma unroll
         for (int i = 0; i < BLOCKS; ++i)
 #pragma unroll
-          for (int k = 0; k < 32; ++k) sum[i][k] = 0.0f;
-        // the accumulator columns of block i
-        auto col = [&](int i) {
-          const int j = 32 * i;
-          return (uint32_t)(GATED && j >= COLS ? BN / 2 + half * COLS + j - COLS
-                                               : half * COLS + j);
-        };
+          for (int k = 0; k < 16; ++k) sum[i][k] = 0.0f;
         const int parts = (kbs + kFlush - 1) / kFlush + 1;
         for (int part = 0; part < parts; ++part) {
           const int acc = part == parts - 1;
           if (!wait_full(acc)) break;
 #pragma unroll
-          for (int i = 0; i < 2 * BLOCKS; ++i) {
+          for (int i = 0; i < BLOCKS; ++i) {
             float x[16];
-            tmem_ld16(lane_base + (uint32_t)(acc * BN) + col(i / 2) + (i & 1) * 16, x);
+            tmem_ld16(lane_base + (uint32_t)(acc * kAccCols + 16 * half + 32 * i), x);
             tmem_ld_wait();
-            if (i == 2 * BLOCKS - 1) release(acc);
+            if (i == BLOCKS - 1) release(acc);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) sum[i / 2][(i & 1) * 16 + k] += x[k];
+            for (int k = 0; k < 16; ++k) sum[i][k] += x[k];
           }
         }
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < COLS / 32; ++i)
-          finish(32 * i, sum[i], sum[GATED ? i + COLS / 32 : i]);
+        for (int i = 0; i < COLS / 16; ++i)
+          out.block(c0 + 16 * half + 32 * i, sum[i], sum[GATED ? i + COLS / 16 : i]);
       }
     }
   }
@@ -533,7 +605,7 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();  // the pair's MMAs read both shared memories
   tc_fence_after();
-  if (warp == 1) ff_tmem_dealloc<CG>(tmem_base, Cfg::TMEM_COLS);
+  if (warp == 1) ff_tmem_dealloc<CG>(tmem_base, kTmemCols);
 }
 
 // ------------------------------------------------------------------ host side
@@ -562,7 +634,8 @@ bool encode(CUtensorMap *m, const FfOperand &o, int planes, int rows) {
                                  (cuuint64_t)(planes > 1 ? o.plane : o.ld * o.outer) * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1}, estr[3] = {1, 1, 1};
   return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(o.p), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -572,13 +645,24 @@ uint64_t env_u64(const char *name, uint64_t dflt) {
   return v && *v ? std::strtoull(v, nullptr, 10) : dflt;
 }
 
+// A tile: the CTAs that share it, its accumulator columns and the rows of A
+// that each CTA loads.  Of a tile with few rows only those are loaded; the MMA
+// reads what lies behind them in place of the others, which ends in rows of
+// the accumulator that nothing reads.
+struct Choice {
+  int cg, bn, a_rows;
+};
+
+int stage_bytes_of(const Choice &c, int planes) {
+  return planes * (c.a_rows + c.bn / c.cg) * kLine;
+}
+
 template <int P, int CG, int BN, bool GATED>
-int launch_cfg(const FfProduct &q, const DeviceProps &dp, cudaStream_t s) {
-  using Cfg = FfCfg<P, CG, BN, GATED>;
+int launch_cfg(const FfProduct &q, const Choice &ch, const DeviceProps &dp, cudaStream_t s) {
   FfParams p{};
   p.M = q.M;
   p.N = q.N;
-  p.kb = (int)ceil_div(q.K, Cfg::BK);
+  p.kb = (int)ceil_div(q.K, kBlockK);
   p.segs = q.kind == kFfConcat ? 2 : 1;
   p.batches = q.kind == kFfBatch ? 2 : 1;
   p.a_seg = p.b_seg = q.kind == kFfConcat;
@@ -598,36 +682,48 @@ int launch_cfg(const FfProduct &q, const DeviceProps &dp, cudaStream_t s) {
   p.wait_ns = env_u64("GEMM_DEBUG_WAIT_LIMIT_NS", 2000000000ull);
   p.stall_producer = (int)env_u64("GEMM_DEBUG_STALL_PRODUCER", 0);
   p.tiles_m = (int)ceil_div(q.M, CG * 128);
-  p.tiles_n = (int)ceil_div(q.N, Cfg::OUT_COLS);
+  p.bn = ch.bn;
+  p.out_cols = GATED ? ch.bn / 2 : ch.bn;
+  p.a_bytes = ch.a_rows * kLine;
+  p.b_bytes = ch.bn / CG * kLine;
+  const int stage = stage_bytes_of(ch, P);
+  p.stages = kStageBudget / stage < kMaxStages ? kStageBudget / stage : kMaxStages;
+  const int smem = p.stages * stage + 1024 + 256 + kEpiBytes;
+  p.tiles_n = (int)ceil_div(q.N, p.out_cols);
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.batches;
   int64_t workers = dp.sm_count / CG;
   if (workers > tiles) workers = tiles;
   p.group_n = p.tiles_n < 8 ? p.tiles_n : 8;
 
+  // columns of B one load brings: the gated form takes each half of a single
+  // CTA's columns, or all of one CTA of a pair, from one of the two matrices
+  const int b_load = GATED && CG == 1 ? ch.bn / 2 : ch.bn / CG;
   CUtensorMap ma[2], mb[2];
   for (int i = 0; i < 2; ++i) {
     const FfOperand &a = q.a[i].p ? q.a[i] : q.a[0], &b = q.b[i].p ? q.b[i] : q.b[0];
-    if (!encode(&ma[i], a, P, a.mn_major ? 64 : 128) ||
-        !encode(&mb[i], b, P, b.mn_major ? 64 : Cfg::B_LOAD))
+    if (!encode(&ma[i], a, P, a.mn_major ? 64 : ch.a_rows) ||
+        !encode(&mb[i], b, P, b.mn_major ? 64 : b_load))
       return GEMM_ERR_UNSUPPORTED;
   }
   auto kern = ff_tc_kernel<P, CG, BN, GATED>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) !=
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
       cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CG;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(workers * CG));
   lc.blockDim = dim3(kThreadsFF);
-  lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+  lc.dynamicSmemBytes = smem;
   lc.stream = s;
   lc.attrs = attr;
-  lc.numAttrs = 1;
+  lc.numAttrs = 2;
   if (cudaLaunchKernelEx(&lc, kern, ma[0], ma[1], mb[0], mb[1], p) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
@@ -635,14 +731,66 @@ int launch_cfg(const FfProduct &q, const DeviceProps &dp, cudaStream_t s) {
   return GEMM_OK;
 }
 
+// Estimated clocks of one tile.  An MMA (16 along K) takes bn / 2 clocks, or
+// what shared memory needs at 128 bytes a clock for its reads (128 rows of A,
+// the CTA's part of B) and for the copies' writes, which serve the one or six
+// products of their planes.  (GB300: three planes of 128 x 128 ran at 94
+// clocks, 256 x 256 at 128.)  A CTA's loads come at about 55 bytes a clock
+// with the ring full of requests (one token, 128 KB in flight: 28 bytes with
+// half of that).  At the end of a CTA's last tile comes an epilogue that
+// nothing hides.
+double tile_clocks(const Choice &c, int planes, double kbs) {
+  const double products = planes == 1 ? 1 : 6, rows = 128 + c.bn / c.cg;
+  const double mma = 4 * products * c.bn / 2.0;
+  const double smem = 4 * products * rows * 32 / 128 + stage_bytes_of(c, planes) / 128.0;
+  const double load = stage_bytes_of(c, planes) / 55.0;
+  const double most = mma > smem ? mma : smem;
+  return kbs * (most > load ? most : load);
+}
+
+// The tile with the least estimated time.  Three planes come in a few sizes,
+// one plane in every width that its operands' storage lets TMA cut: blocks of
+// 16 output columns, MN-major ones of 64, from one matrix or one half.
+Choice choose(const FfProduct &q, int sms) {
+  const bool gated = q.kind == kFfGated;
+  const double kbs = (double)ceil_div(q.K, kBlockK) * (q.kind == kFfConcat ? 2 : 1);
+  Choice best{};
+  double least = 0.0;
+  for (int cg = 2; cg >= 1; --cg) {
+    const int parts = gated || cg == 2 ? 2 : 1;  // loads that share the columns
+    const int unit = q.b[0].mn_major ? 64 * parts : gated || cg == 2 ? 32 : 16;
+    for (int bn = 256; bn >= 32; bn -= 16) {
+      if (bn % unit != 0) continue;
+      if (q.planes == 3 && bn != 256 && bn != 128 && bn != 64) continue;
+      if (q.planes == 3 && (cg == 2 ? bn == 64 : bn == 256 || (gated && bn == 64))) continue;
+      const int a_rows = cg == 1 && !q.a[0].mn_major && q.M < 128 ? (int)ceil_div(q.M, 8) * 8 : 128;
+      const Choice c{cg, bn, a_rows};
+      const int64_t tiles = ceil_div(q.M, cg * 128) * ceil_div(q.N, gated ? bn / 2 : bn) *
+                            (q.kind == kFfBatch ? 2 : 1);
+      const double t = (double)ceil_div(tiles, sms / cg) * tile_clocks(c, q.planes, kbs) + 30.0 * bn;
+      if (least == 0.0 || t < least) {
+        least = t;
+        best = c;
+      }
+    }
+  }
+  return best;
+}
+
 template <int P, bool GATED>
 int launch_any(const FfProduct &q, const DeviceProps &dp, cudaStream_t s) {
-  // Tiles of 256 x 256 by pairs of CTAs once they fill the GPU, 128 x 128 by
-  // single ones otherwise.
-  const int64_t out = GATED ? 128 : 256;
-  const int64_t big = ceil_div(q.M, 256) * ceil_div(q.N, out) * (q.kind == kFfBatch ? 2 : 1);
-  if (big >= dp.sm_count / 2) return launch_cfg<P, 2, 256, GATED>(q, dp, s);
-  return launch_cfg<P, 1, 128, GATED>(q, dp, s);
+  const Choice c = choose(q, dp.sm_count);
+  if constexpr (P == 1) {
+    return c.cg == 2 ? launch_cfg<1, 2, 0, GATED>(q, c, dp, s)
+                     : launch_cfg<1, 1, 0, GATED>(q, c, dp, s);
+  } else {
+    if (c.cg == 2)
+      return c.bn == 256 ? launch_cfg<3, 2, 256, GATED>(q, c, dp, s)
+                         : launch_cfg<3, 2, 128, GATED>(q, c, dp, s);
+    if constexpr (!GATED)
+      if (c.bn == 64) return launch_cfg<3, 1, 64, false>(q, c, dp, s);
+    return launch_cfg<3, 1, 128, GATED>(q, c, dp, s);
+  }
 }
 
 }  // namespace

@@ -43,7 +43,10 @@ __global__ void __launch_bounds__(128) q4_kernel(Q4Args p) {
   if (n >= p.N) return;
   for (int64_t m = 0; m < p.M; ++m) {
     float y = q4_dot<T>(p, p.w[0], m, n);
-    if (GATED) y = act_value<false>(y, p.act) * q4_dot<T>(p, p.w[1], m, n);
+    if (GATED) {
+      const float u = q4_dot<T>(p, p.w[1], m, n);
+      with_act(p.act, [&](auto a) { y = act_of<false, decltype(a)::value>(y) * u; });
+    }
     if ((threadIdx.x & 31) == 0) static_cast<T *>(p.y)[m * p.ldy + n] = from_f32<T>(y);
   }
 }

@@ -8,6 +8,9 @@ rules of each call).  Tensors are torch CUDA tensors, float32 or bfloat16.
 from __future__ import annotations
 
 import ctypes
+from array import array
+
+import torch
 
 from . import gemm
 from .gemm import GemmError, OK, OP_N, OP_T
@@ -29,67 +32,79 @@ def _act(act) -> int:
     return int(act)
 
 
-_DTYPES = {}
+_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
 
 
 def _dtype(t) -> int:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: DT_F32, torch.bfloat16: DT_BF16})
     d = _DTYPES.get(t.dtype)
     if d is None:
         raise ValueError(f"dtype {t.dtype}: float32 or bfloat16 wanted")
     return d
 
 
-def _rows(t, name, like=None, shape=None, dtype=None):
-    """Leading dimension of a row-major 2-D CUDA tensor."""
-    if not t.is_cuda or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    if like is not None and (t.dtype != (dtype or like.dtype) or t.device != like.device):
-        raise ValueError(f"{name} must be {dtype or like.dtype} on the first operand's device")
-    r, c = t.shape
-    if shape is not None and (r, c) != shape:
-        raise ValueError(f"{name} is {r} x {c}, {shape[0]} x {shape[1]} wanted")
+def _rows(t, name, rows, cols, dtype, device):
+    """Leading dimension of a row-major rows x cols matrix."""
+    if t.shape != (rows, cols) or t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be {rows} x {cols}, {dtype}, on CUDA device {device}: got "
+                         f"{tuple(t.shape)}, {t.dtype}, {t.device}")
     s0, s1 = t.stride()
-    if s1 != 1 and c > 1:
+    if s1 != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     # the row stride of a one-row matrix is never used
-    return max(s0 if r > 1 else c, 1)
+    return (s0 if rows > 1 else cols) or 1
 
 
-def _weight(t, name, like, D, F):
+def _first(t, name):
+    """(rows, cols, leading dimension, dtype code, device index) of the matrix that sets them."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    rows, cols = t.shape
+    device = t.get_device()
+    return rows, cols, _rows(t, name, rows, cols, t.dtype, device), _dtype(t), device
+
+
+def _weight(t, name, D, F, dtype, device):
     """{op: ld} of the ways a D x F weight can be read: row-major is op N,
     ``W.t()`` of a stored F x D matrix op T (one row or column may be either)."""
-    if not t.is_cuda or t.dim() != 2 or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor of the first operand's dtype and device")
-    if tuple(t.shape) != (D, F):
-        raise ValueError(f"{name} is {tuple(t.shape)}, {(D, F)} wanted")
+    if t.shape != (D, F) or t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be {D} x {F}, {dtype}, on CUDA device {device}: got "
+                         f"{tuple(t.shape)}, {t.dtype}, {t.device}")
     s0, s1 = t.stride()
     ops = {}
     if s1 == 1 or F <= 1:
-        ops[OP_N] = max(s0 if D > 1 else F, 1)
+        ops[OP_N] = (s0 if D > 1 else F) or 1
     if s0 == 1 or D <= 1:
-        ops[OP_T] = max(s1 if F > 1 else D, 1)
+        ops[OP_T] = (s1 if F > 1 else D) or 1
     if not ops:
         raise ValueError(f"{name} must have a unit row or column stride")
     return ops
 
 
-def _weights(Wg, Wu, like, D, F):
-    g, u = _weight(Wg, "Wg", like, D, F), _weight(Wu, "Wu", like, D, F)
+def _weights(Wg, Wu, D, dtype, device):
+    """(F, op, ld of Wg, ld of Wu)."""
+    if Wg.dim() != 2:
+        raise ValueError("Wg must be a 2-D tensor")
+    F = Wg.shape[1]
+    g, u = _weight(Wg, "Wg", D, F, dtype, device), _weight(Wu, "Wu", D, F, dtype, device)
     for op in (OP_N, OP_T):
         if op in g and op in u:
-            return op, g[op], u[op]
+            return F, op, g[op], u[op]
     raise ValueError("Wg and Wu must be stored in the same order")
 
 
-def _stream(stream, *new):
+def _matrix(rows, cols, dtype, device, order=OP_N, pad=False):
+    """A new rows x cols matrix, row-major or (OP_T) the transpose of one;
+    ``pad``: with rows on 16-byte boundaries."""
+    ld = -(-cols // 8) * 8 if pad else cols
+    return torch.empty_strided((rows, cols), (ld, 1) if order == OP_N else (1, rows), dtype=dtype,
+                               device=device)
+
+
+def _stream(stream, device, *new):
     """The handle to launch on.  Tensors made here on torch's current stream
     and used on another are told so, for the caching allocator."""
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device)
     for t in new:
         if t is not None:
             t.record_stream(stream)
@@ -98,6 +113,10 @@ def _stream(stream, *new):
 
 def _workspace(w):
     return (None, 0) if w is None else (w.data_ptr(), w.numel() * w.element_size())
+
+
+def _lib():
+    return gemm._lib or gemm.load()
 
 
 def _check(rc, what):
@@ -111,23 +130,22 @@ def gated_ff(X, Wg, Wu, act="silu", save=False, out=None, stream=None, workspace
     ``save`` (H, G, U), where G = X @ Wg and U = X @ Wu, in float32, are what
     ``gated_ff_backward`` reads.  ``workspace``: as for ``gemm.matmul``
     (``gated_ff_workspace`` bytes)."""
-    import torch
-    M, D = X.shape
-    F = Wg.shape[1]
-    dt, ldx = _dtype(X), _rows(X, "X")
-    op, ldg, ldu = _weights(Wg, Wu, X, D, F)
-    H = torch.empty((M, F), dtype=X.dtype, device=X.device) if out is None else out
-    ldh = F if out is None else _rows(out, "out", X, (M, F))
-    G = U = None
+    M, D, ldx, dt, dev = _first(X, "X")
+    dtype, device = X.dtype, X.device
+    F, op, ldwg, ldwu = _weights(Wg, Wu, D, dtype, dev)
+    H = _matrix(M, F, dtype, device) if out is None else out
+    ldh = (F or 1) if out is None else _rows(out, "out", M, F, dtype, dev)
+    G = U = g = u = None
     if save:
-        G = torch.empty((M, F), dtype=torch.float32, device=X.device)
-        U = torch.empty((M, F), dtype=torch.float32, device=X.device)
+        G = _matrix(M, F, torch.float32, device, pad=True)
+        U = _matrix(M, F, torch.float32, device, pad=True)
+        g, u = G.data_ptr(), U.data_ptr()
+    lds = -(-(F or 1) // 8) * 8
     ws, wsb = _workspace(workspace)
-    _check(gemm.load().gated_ff(
-        dt, _act(act), op, M, D, F, X.data_ptr(), ldx, Wg.data_ptr(), ldg, Wu.data_ptr(), ldu,
-        H.data_ptr(), max(ldh, 1), G.data_ptr() if save else None, max(F, 1),
-        U.data_ptr() if save else None, max(F, 1), ws, wsb,
-        _stream(stream, None if out is not None else H, G, U)), "gated_ff")
+    rc = _lib().gated_ff(dt, _act(act), op, M, D, F, X.data_ptr(), ldx, Wg.data_ptr(), ldwg,
+                         Wu.data_ptr(), ldwu, H.data_ptr(), ldh, g, lds, u, lds, ws, wsb,
+                         _stream(stream, dev, None if out is not None else H, G, U))
+    _check(rc, "gated_ff")
     return (H, G, U) if save else H
 
 
@@ -137,131 +155,129 @@ def gated_ff_backward(dH, X, Wg, Wu, G, U, act="silu", need_dx=True, need_dw=Tru
     weights' gradients are stored as the weights are (for a weight passed as
     ``W.t()``, dWg.t() is the contiguous F x D gradient of W).  What is not
     needed is None."""
-    import torch
-    M, D = X.shape
-    F = Wg.shape[1]
-    dt, ldx = _dtype(X), _rows(X, "X")
-    op, ldg, ldu = _weights(Wg, Wu, X, D, F)
-    lds = [_rows(dH, "dH", X, (M, F)), _rows(G, "G", X, (M, F), torch.float32),
-           _rows(U, "U", X, (M, F), torch.float32)]
-    dX = dWg = dWu = None
+    M, D, ldx, dt, dev = _first(X, "X")
+    dtype, device = X.dtype, X.device
+    F, op, ldwg, ldwu = _weights(Wg, Wu, D, dtype, dev)
+    ldh = _rows(dH, "dH", M, F, dtype, dev)
+    ldg = _rows(G, "G", M, F, torch.float32, dev)
+    ldu = _rows(U, "U", M, F, torch.float32, dev)
+    dX = dWg = dWu = dx = dg = du = None
     if need_dx:
-        dX = torch.empty((M, D), dtype=X.dtype, device=X.device)
+        dX = _matrix(M, D, dtype, device)
+        dx = dX.data_ptr()
     if need_dw:
-        shape = (D, F) if op == OP_N else (F, D)
-        dWg = torch.empty(shape, dtype=X.dtype, device=X.device)
-        dWu = torch.empty(shape, dtype=X.dtype, device=X.device)
-    ldw = max(F if op == OP_N else D, 1)
+        dWg, dWu = _matrix(D, F, dtype, device, op), _matrix(D, F, dtype, device, op)
+        dg, du = dWg.data_ptr(), dWu.data_ptr()
+    ldw = (F if op == OP_N else D) or 1
     ws, wsb = _workspace(workspace)
     if need_dx or need_dw:
-        _check(gemm.load().gated_ff_backward(
-            dt, _act(act), op, M, D, F, dH.data_ptr(), lds[0], X.data_ptr(), ldx, Wg.data_ptr(),
-            ldg, Wu.data_ptr(), ldu, G.data_ptr(), lds[1], U.data_ptr(), lds[2],
-            dX.data_ptr() if need_dx else None, max(D, 1), dWg.data_ptr() if need_dw else None,
-            ldw, dWu.data_ptr() if need_dw else None, ldw, ws, wsb,
-            _stream(stream, dX, dWg, dWu)), "gated_ff_backward")
-    if need_dw and op == OP_T:
-        dWg, dWu = dWg.t(), dWu.t()
+        rc = _lib().gated_ff_backward(
+            dt, _act(act), op, M, D, F, dH.data_ptr(), ldh, X.data_ptr(), ldx, Wg.data_ptr(),
+            ldwg, Wu.data_ptr(), ldwu, G.data_ptr(), ldg, U.data_ptr(), ldu, dx, D or 1, dg, ldw,
+            du, ldw, ws, wsb, _stream(stream, dev, dX, dWg, dWu))
+        _check(rc, "gated_ff_backward")
     return dX, dWg, dWu
 
 
 def gated_ff_workspace(M, D, F, dtype, op_w=OP_N, backward=False, aligned=False) -> int:
     """Scratch bytes a call of these sizes may need (dtype: DT_F32 or DT_BF16)."""
     out = ctypes.c_uint64(0)
-    _check(gemm.load().gated_ff_workspace(1 if backward else 0, dtype, op_w, M, D, F,
+    _check(_lib().gated_ff_workspace(1 if backward else 0, dtype, op_w, M, D, F,
                                           1 if aligned else 0, ctypes.byref(out)),
            "gated_ff_workspace")
     return out.value
 
 
-def _q4_side(q, s, z, like, K, group, name):
-    """(q, ldq, s, z) addresses of one quantised matrix, checked against K and group."""
-    N = q.shape[0]
-    if not q.is_cuda or q.dim() != 2 or q.element_size() != 1 or q.shape[1] != (K + 1) // 2:
-        raise ValueError(f"{name} must be an N x {(K + 1) // 2} uint8 CUDA tensor")
-    if q.shape[1] > 1 and q.stride(1) != 1:
+def _q4_side(q, s, z, dtype, device, K, group, name):
+    """(codes, ldq, scales, zero points) of one quantised matrix, checked against K and group."""
+    N, width = q.shape
+    if q.dtype != torch.uint8 or q.get_device() != device or width != (K + 1) // 2:
+        raise ValueError(f"{name} must be N x {(K + 1) // 2}, uint8, on CUDA device {device}")
+    ldq, one = q.stride()
+    if one != 1 and width > 1:
         raise ValueError(f"{name} must have unit column stride")
-    groups = -(-K // group)
+    shape = (N, -(-K // group))
     for t, what in ((s, "scales"), (z, "zeros")):
-        if t is not None and (t.dtype != like.dtype or not t.is_cuda or
-                              tuple(t.shape) != (N, groups) or not t.is_contiguous()):
-            raise ValueError(f"{what} of {name} must be contiguous, {N} x {groups}, of X's dtype")
-    ldq = q.stride(0) if N > 1 else q.shape[1]
-    return q.data_ptr(), max(ldq, 1), s.data_ptr(), None if z is None else z.data_ptr()
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.get_device() != device or
+                              not t.is_contiguous()):
+            raise ValueError(f"{what} of {name} must be {shape[0]} x {shape[1]}, contiguous, "
+                             f"{dtype}, on CUDA device {device}")
+    return (q.data_ptr(), (ldq if N > 1 else width) or 1, s.data_ptr(),
+            None if z is None else z.data_ptr())
 
 
 def q4_matmul(X, Wq, scales, zeros=None, group=128, out=None, stream=None):
     """Y = X @ W.t() with W (N x K) in 4-bit codes: Wq uint8 N x ceil(K/2), the
     even column's code in the low half of each byte; W(n,k) =
     scales(n, k // group) * (code - zeros(n, k // group)), zeros 8 when None."""
-    import torch
-    M, K = X.shape
-    N = Wq.shape[0]
-    if group <= 0:
-        raise ValueError("group must be positive")
-    w = _q4_side(Wq, scales, zeros, X, K, group, "Wq")
-    Y = torch.empty((M, N), dtype=X.dtype, device=X.device) if out is None else out
-    ldy = max(N, 1) if out is None else _rows(out, "out", X, (M, N))
-    _check(gemm.load().q4_matmul(_dtype(X), M, N, K, X.data_ptr(), _rows(X, "X"), *w, group,
-                                 Y.data_ptr(), ldy, _stream(stream, None if out is not None else Y)),
-           "q4_matmul")
+    M, K, ldx, dt, dev = _first(X, "X")
+    if group <= 0 or Wq.dim() != 2:
+        raise ValueError("group must be positive and Wq a 2-D tensor")
+    N, dtype = Wq.shape[0], X.dtype
+    q, ldq, s, z = _q4_side(Wq, scales, zeros, dtype, dev, K, group, "Wq")
+    Y = torch.empty((M, N), dtype=dtype, device=X.device) if out is None else out
+    ldy = (N or 1) if out is None else _rows(out, "out", M, N, dtype, dev)
+    _check(_lib().q4_matmul(dt, M, N, K, X.data_ptr(), ldx, q, ldq, s, z, group, Y.data_ptr(), ldy,
+                            _stream(stream, dev, None if out is not None else Y)), "q4_matmul")
     return Y
 
 
 def q4_gated(X, Wq_g, scales_g, Wq_u, scales_u, zeros_g=None, zeros_u=None, group=128,
              act="silu", out=None, stream=None):
     """H = act(X @ Wg.t()) * (X @ Wu.t()), both weights in the format of ``q4_matmul``."""
-    import torch
-    M, K = X.shape
-    N = Wq_g.shape[0]
-    if group <= 0:
-        raise ValueError("group must be positive")
+    M, K, ldx, dt, dev = _first(X, "X")
+    if group <= 0 or Wq_g.dim() != 2 or Wq_u.dim() != 2:
+        raise ValueError("group must be positive, Wq_g and Wq_u 2-D tensors")
+    N, dtype = Wq_g.shape[0], X.dtype
     if Wq_u.shape[0] != N:
         raise ValueError("Wq_g and Wq_u must have the same number of rows")
-    g = _q4_side(Wq_g, scales_g, zeros_g, X, K, group, "Wq_g")
-    u = _q4_side(Wq_u, scales_u, zeros_u, X, K, group, "Wq_u")
-    H = torch.empty((M, N), dtype=X.dtype, device=X.device) if out is None else out
-    ldh = max(N, 1) if out is None else _rows(out, "out", X, (M, N))
-    _check(gemm.load().q4_gated(_dtype(X), _act(act), M, N, K, X.data_ptr(), _rows(X, "X"), *g,
-                                *u, group, H.data_ptr(), ldh,
-                                _stream(stream, None if out is not None else H)), "q4_gated")
+    g = _q4_side(Wq_g, scales_g, zeros_g, dtype, dev, K, group, "Wq_g")
+    u = _q4_side(Wq_u, scales_u, zeros_u, dtype, dev, K, group, "Wq_u")
+    H = torch.empty((M, N), dtype=dtype, device=X.device) if out is None else out
+    ldh = (N or 1) if out is None else _rows(out, "out", M, N, dtype, dev)
+    _check(_lib().q4_gated(dt, _act(act), M, N, K, X.data_ptr(), ldx, *g, *u, group, H.data_ptr(),
+                           ldh, _stream(stream, dev, None if out is not None else H)), "q4_gated")
     return H
 
 
 def _tensors(ts, name):
-    """(addresses, sizes, dtypes) of a list of contiguous CUDA tensors."""
-    for t in ts:
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous CUDA tensors")
-    return [t.data_ptr() for t in ts], [t.numel() for t in ts], [_dtype(t) for t in ts]
+    """(device, addresses, sizes, dtype codes) of a list of contiguous CUDA tensors."""
+    if not all(map(torch.Tensor.is_contiguous, ts)):
+        raise ValueError(f"{name} must be contiguous tensors")
+    devices = set(map(torch.Tensor.get_device, ts))
+    if len(devices) > 1 or -1 in devices:
+        raise ValueError(f"{name} must be CUDA tensors of one device")
+    try:
+        dts = [_DTYPES[t.dtype] for t in ts]
+    except KeyError as e:
+        raise ValueError(f"dtype {e.args[0]} in {name}: float32 or bfloat16 wanted") from None
+    return (devices.pop() if devices else None, array("Q", map(torch.Tensor.data_ptr, ts)),
+            array("q", map(torch.Tensor.numel, ts)), array("i", dts))
 
 
 def _norm_clip(grads, max_norm, outs, stream, workspace):
-    import torch
-    n = len(grads)
-    ptrs, sizes, dts = _tensors(grads, "grads")
+    device, ptrs, sizes, dts = _tensors(grads, "grads")
     optrs = None
-    if outs is not None:
-        if outs is grads:
-            optrs = ptrs
-        else:
-            optrs, osizes, odts = _tensors(outs, "out")
-            if osizes != sizes or odts != dts:
-                raise ValueError("out must match grads in number, sizes and dtypes")
-    device = grads[0].device if n else "cuda"
-    norm = torch.empty((), dtype=torch.float32, device=device)
-    vp, i64 = ctypes.c_void_p * n, ctypes.c_int64 * n
+    if outs is grads:
+        optrs = ptrs
+    elif outs is not None:
+        odev, optrs, osizes, odts = _tensors(outs, "out")
+        if odev != device or osizes != sizes or odts != dts:
+            raise ValueError("out must match grads in number, sizes, dtypes and device")
+    if device is None:
+        device = torch.cuda.current_device()
+    norm = torch.empty((), dtype=torch.float32, device=f"cuda:{device}")
+    at = lambda a: None if a is None else a.buffer_info()[0]  # noqa: E731
     ws, wsb = _workspace(workspace)
-    _check(gemm.load().grad_norm_clip(n, (ctypes.c_int * n)(*dts), vp(*ptrs),
-                                      None if optrs is None else vp(*optrs), i64(*sizes),
-                                      float(max_norm), norm.data_ptr(), ws, wsb,
-                                      _stream(stream, norm)), "grad_norm_clip")
+    _check(_lib().grad_norm_clip(len(ptrs), at(dts), at(ptrs), at(optrs), at(sizes),
+                                 float(max_norm), norm.data_ptr(), ws, wsb,
+                                 _stream(stream, device, norm)), "grad_norm_clip")
     return norm
 
 
 def grad_norm(grads, stream=None, workspace=None):
     """sqrt of the sum of squares over all tensors, as a 0-d float32 tensor."""
-    return _norm_clip(grads, 0.0, None, stream, workspace)
+    return _norm_clip(list(grads), 0.0, None, stream, workspace)
 
 
 def clip_grad_norm(grads, max_norm, out=None, stream=None, workspace=None):
