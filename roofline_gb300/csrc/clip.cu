@@ -1,6 +1,14 @@
 // The global gradient norm over many tensors, and clipping by it
 // (include/gb300_gemm.h, grad_norm_clip).
+//
+// Two kernels: the sum of squares, and the scaling, which adds the blocks'
+// sums in a fixed order first.  Both are bound by HBM: every gradient is read
+// twice (a set larger than L2 cannot wait on the chip for the norm) and
+// written once.  The tensors are cut into chunks of 16 KB; a block takes a
+// run of neighbouring chunks, in the second kernel backwards, so that it
+// begins with what the first one left in L2.
 #include "ff.cuh"
+#include "tc_common.cuh"
 
 namespace gg {
 namespace {
@@ -11,21 +19,56 @@ struct ClipTensor {
   const void *in;
   void *out;
   int64_t n;
-  int64_t dtype;
+  int32_t first, dtype;  // its first chunk among the table's
 };
-constexpr int kClipTable = 1000;  // tensors of one launch
+template <int N>
 struct ClipTable {
-  int count;
-  ClipTensor t[kClipTable];
+  int count, chunks;
+  ClipTensor t[N];
 };
-constexpr int kClipBlocks = 608, kClipThreads = 256;
+constexpr int kClipSmall = 64, kClipTable = 1000;  // tensors of one launch
+constexpr int kClipThreads = 256, kClipVectors = 4;
+constexpr int kClipChunk = kClipThreads * kClipVectors;  // 16-byte vectors of a chunk
+constexpr int kClipBlocksPerSm = 8;
 
-__device__ __forceinline__ float clip_load(const ClipTensor &t, int64_t i) {
-  return t.dtype == GEMM_DT_F32 ? static_cast<const float *>(t.in)[i]
-                                : to_f32(static_cast<const bf16 *>(t.in)[i]);
+// The elements of a tensor before its first 16-byte boundary.
+__host__ __device__ __forceinline__ int64_t clip_head(const void *p, int64_t n, int size) {
+  const int64_t head = (16 - (int64_t)(reinterpret_cast<uintptr_t>(p) & 15)) % 16 / size;
+  return head < n ? head : n;
+}
+__host__ __device__ __forceinline__ int64_t clip_vectors(const void *p, int64_t n, int size) {
+  return (n - clip_head(p, n, size)) / (16 / size);
 }
 
-// The block's sum of v, in a fixed order, in thread 0.
+// The tensor of chunk `c`.
+template <int N>
+__device__ __forceinline__ int clip_find(const ClipTable<N> &tab, int c) {
+  int lo = 0, hi = tab.count - 1;  // the last tensor that begins at or before c
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (tab.t[mid].first <= c)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+template <typename T>
+__device__ __forceinline__ void clip_unpack(const uint4 &v, float (&x)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      x[i] = __uint_as_float(w[i]);
+    } else {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+// The block's sum of v, in a fixed order, in every thread.
 __device__ double block_sum(double v) {
   __shared__ double part[kClipThreads / 32];
 #pragma unroll
@@ -33,52 +76,229 @@ __device__ double block_sum(double v) {
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0.0;
-  if (threadIdx.x == 0)
-    for (int w = 0; w < kClipThreads / 32; ++w) v += part[w];
+#pragma unroll
+  for (int w = 0; w < kClipThreads / 32; ++w) v += part[w];
   __syncthreads();
   return v;
 }
 
-__global__ void __launch_bounds__(kClipThreads)
-clip_sum_kernel(const __grid_constant__ ClipTable tab, double *partial) {
-  double sum = 0.0;
-  for (int k = 0; k < tab.count; ++k) {
-    const ClipTensor &t = tab.t[k];
-    for (int64_t i = blockIdx.x * (int64_t)kClipThreads + threadIdx.x; i < t.n;
-         i += (int64_t)kClipBlocks * kClipThreads) {
-      const double x = clip_load(t, i);
-      sum += x * x;
-    }
+// Sum of the squares of a thread's values: in FP32 where that neither
+// overflows nor underflows, else with the values scaled by a power of two.
+template <typename F>
+__device__ __forceinline__ double squares(F sum_scaled) {
+  const float s = sum_scaled(1.0f);
+  if (s >= 0x1p-80f && s <= 0x1p100f) return (double)s;
+  if (s < 0x1p-80f) return (double)sum_scaled(0x1p64f) * 0x1p-128;
+  return (double)sum_scaled(0x1p-96f) * 0x1p192;  // Inf and NaN stay what they are
+}
+
+template <typename T>
+__device__ __forceinline__ double clip_chunk_sum(const ClipTensor &t, int64_t v0) {
+  constexpr int VE = 16 / sizeof(T);
+  const T *in = static_cast<const T *>(t.in);
+  const int64_t head = clip_head(in, t.n, sizeof(T)), vectors = (t.n - head) / VE;
+  const uint4 *vec = reinterpret_cast<const uint4 *>(in + head);
+  uint4 r[kClipVectors];
+#pragma unroll
+  for (int j = 0; j < kClipVectors; ++j) {
+    const int64_t v = v0 + j * kClipThreads + threadIdx.x;
+    r[j] = v < vectors ? __ldg(vec + v) : make_uint4(0, 0, 0, 0);
   }
+  double sum = squares([&](float scale) {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kClipVectors; ++j) {
+      float x[VE];
+      clip_unpack<T>(r[j], x);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float y = x[i] * scale;
+        s = fmaf(y, y, s);
+      }
+    }
+    return s;
+  });
+  // the elements before the first vector and behind the last
+  if (v0 == 0 && threadIdx.x < head) {
+    const double x = to_f32(in[threadIdx.x]);
+    sum += x * x;
+  }
+  const int64_t tail = head + vectors * VE + threadIdx.x;
+  if (v0 + kClipChunk >= vectors && tail < t.n) {
+    const double x = to_f32(in[tail]);
+    sum += x * x;
+  }
+  return sum;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kClipThreads)
+clip_sum_kernel(const __grid_constant__ ClipTable<N> tab, double *partial) {
+  tc::grid_dependency_wait();
+  const int c0 = (int)((int64_t)tab.chunks * blockIdx.x / gridDim.x);
+  const int c1 = (int)((int64_t)tab.chunks * (blockIdx.x + 1) / gridDim.x);
+  double sum = 0.0;
+  int k = clip_find(tab, c0);
+  for (int c = c0; c < c1; ++c) {
+    while (k + 1 < tab.count && tab.t[k + 1].first <= c) ++k;
+    const ClipTensor &t = tab.t[k];
+    const int64_t v0 = (int64_t)(c - t.first) * kClipChunk;
+    sum += t.dtype == GEMM_DT_F32 ? clip_chunk_sum<float>(t, v0) : clip_chunk_sum<bf16>(t, v0);
+  }
+  tc::grid_launch_dependents();
   sum = block_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(kClipThreads)
-clip_norm_kernel(const double *partial, int64_t n, float *norm) {
+__device__ float clip_norm(const double *partial, int count) {
   double sum = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += kClipThreads) sum += partial[i];
-  sum = block_sum(sum);
-  if (threadIdx.x == 0) *norm = (float)sqrt(sum);
+  for (int i = threadIdx.x; i < count; i += kClipThreads) sum += partial[i];
+  return (float)sqrt(block_sum(sum));
 }
 
 __global__ void __launch_bounds__(kClipThreads)
-clip_scale_kernel(const __grid_constant__ ClipTable tab, const float *norm, float max_norm) {
-  const float r = max_norm / (*norm + 1e-6f);
-  const float c = r < 1.0f || r != r ? r : 1.0f;
-  for (int k = 0; k < tab.count; ++k) {
-    const ClipTensor &t = tab.t[k];
-    for (int64_t i = blockIdx.x * (int64_t)kClipThreads + threadIdx.x; i < t.n;
-         i += (int64_t)kClipBlocks * kClipThreads) {
-      const float x = clip_load(t, i) * c;
-      if (t.dtype == GEMM_DT_F32)
-        static_cast<float *>(t.out)[i] = x;
-      else
-        static_cast<bf16 *>(t.out)[i] = from_f32<bf16>(x);
+clip_norm_kernel(const double *partial, int count, float *norm) {
+  tc::grid_dependency_wait();
+  const float n = clip_norm(partial, count);
+  if (threadIdx.x == 0) *norm = n;
+}
+
+template <typename T>
+__device__ __forceinline__ void clip_chunk_scale(const ClipTensor &t, int64_t v0, float c) {
+  constexpr int VE = 16 / sizeof(T);
+  const T *in = static_cast<const T *>(t.in);
+  T *out = static_cast<T *>(t.out);
+  const int64_t head = clip_head(in, t.n, sizeof(T)), vectors = (t.n - head) / VE;
+  auto scaled = [&](float x) { return from_f32<T>(x * c); };
+  if ((((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0)) {
+    const uint4 *vec = reinterpret_cast<const uint4 *>(in + head);
+    uint4 *dst = reinterpret_cast<uint4 *>(out + head);
+    uint4 r[kClipVectors];
+#pragma unroll
+    for (int j = 0; j < kClipVectors; ++j) {
+      const int64_t v = v0 + j * kClipThreads + threadIdx.x;
+      r[j] = v < vectors ? vec[v] : make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int j = 0; j < kClipVectors; ++j) {
+      const int64_t v = v0 + j * kClipThreads + threadIdx.x;
+      float x[VE];
+      clip_unpack<T>(r[j], x);
+      __align__(16) T y[VE];
+#pragma unroll
+      for (int i = 0; i < VE; ++i) y[i] = scaled(x[i]);
+      if (v < vectors) dst[v] = *reinterpret_cast<const uint4 *>(y);
+    }
+  } else {
+    // out is aligned otherwise: element by element
+    const int64_t e1 = head + (v0 + kClipChunk < vectors ? v0 + kClipChunk : vectors) * VE;
+#pragma unroll 4
+    for (int64_t e = head + v0 * VE + threadIdx.x; e < e1; e += kClipThreads)
+      out[e] = scaled(to_f32(in[e]));
+  }
+  if (v0 == 0 && threadIdx.x < head) out[threadIdx.x] = scaled(to_f32(in[threadIdx.x]));
+  const int64_t tail = head + vectors * VE + threadIdx.x;
+  if (v0 + kClipChunk >= vectors && tail < t.n) out[tail] = scaled(to_f32(in[tail]));
+}
+
+template <int N>
+__global__ void __launch_bounds__(kClipThreads)
+clip_scale_kernel(const __grid_constant__ ClipTable<N> tab, const double *partial, int count,
+                  float max_norm, float *norm) {
+  tc::grid_dependency_wait();
+  const float n = clip_norm(partial, count);
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
+  const float r = max_norm / (n + 1e-6f);
+  const float s = r < 1.0f || r != r ? r : 1.0f;
+  const int c0 = (int)((int64_t)tab.chunks * blockIdx.x / gridDim.x);
+  const int c1 = (int)((int64_t)tab.chunks * (blockIdx.x + 1) / gridDim.x);
+  int k = c1 > c0 ? clip_find(tab, c1 - 1) : 0;
+  for (int c = c1 - 1; c >= c0; --c) {
+    while (tab.t[k].first > c) --k;
+    const ClipTensor &t = tab.t[k];
+    if (s == 1.0f && t.in == t.out) continue;  // x * 1 is there already
+    const int64_t v0 = (int64_t)(c - t.first) * kClipChunk;
+    if (t.dtype == GEMM_DT_F32)
+      clip_chunk_scale<float>(t, v0, s);
+    else
+      clip_chunk_scale<bf16>(t, v0, s);
   }
 }
 
+// Launched with programmatic dependent launch: each kernel waits for the one
+// before it before it touches memory.
+template <typename... Params, typename... Args>
+cudaError_t clip_launch(void (*kern)(Params...), int grid, cudaStream_t s, const Args &...args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)grid);
+  lc.blockDim = dim3(kClipThreads);
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kern, Params(args)...);
+}
+
+struct ClipCall {
+  int64_t count;
+  const int *dtypes;
+  const void *const *grads;
+  void *const *outs;
+  const int64_t *sizes;
+  int blocks;  // most of one launch
+  double *partial;
+  float max_norm, *norm;
+  cudaStream_t stream;
+};
+
+// All launches of a call, up to N tensors in each.
+template <int N>
+cudaError_t clip_run(const ClipCall &q) {
+  static thread_local ClipTable<N> tab;
+  // The tensors from `at` on; returns the first that is left.
+  auto fill = [&](int64_t at) {
+    int64_t chunks = 0;
+    tab.count = 0;
+    while (at < q.count && tab.count < N) {
+      const int size = (int)dtype_size(q.dtypes[at]);
+      const int64_t c =
+          ceil_div(clip_vectors(q.grads[at], q.sizes[at], size), kClipChunk);
+      if (q.sizes[at] > 0) {
+        tab.t[tab.count++] = {q.grads[at], q.outs ? q.outs[at] : nullptr, q.sizes[at],
+                              (int32_t)chunks, q.dtypes[at]};
+        chunks += c > 0 ? c : 1;
+      }
+      ++at;
+    }
+    tab.chunks = (int)chunks;
+    return at;
+  };
+  auto grid = [&] { return tab.chunks < q.blocks ? tab.chunks : q.blocks; };
+  int partials = 0;
+  cudaError_t e = cudaSuccess;
+  for (int64_t at = 0; at < q.count && e == cudaSuccess;) {
+    at = fill(at);
+    if (tab.count == 0) continue;
+    e = clip_launch(clip_sum_kernel<N>, grid(), q.stream, tab, q.partial + partials);
+    partials += grid();
+  }
+  if (e != cudaSuccess) return e;
+  if (!q.outs || partials == 0)
+    return clip_launch(clip_norm_kernel, 1, q.stream, q.partial, partials, q.norm);
+  float *norm = q.norm;
+  for (int64_t at = 0; at < q.count && e == cudaSuccess;) {
+    at = fill(at);
+    if (tab.count == 0) continue;
+    e = clip_launch(clip_scale_kernel<N>, grid(), q.stream, tab, q.partial, partials, q.max_norm,
+                    norm);
+    norm = nullptr;  // the first launch writes it
+  }
+  return e;
+}
+
+// Launches of one pass, at most.
 int64_t clip_launches(int64_t count) { return count > 0 ? ceil_div(count, kClipTable) : 0; }
 
 }  // namespace
@@ -89,7 +309,8 @@ using namespace gg;
 extern "C" {
 
 uint64_t grad_norm_clip_workspace(int64_t count) {
-  return (uint64_t)(count > 0 ? clip_launches(count) : 0) * kClipBlocks * sizeof(double);
+  return (uint64_t)clip_launches(count) * current_props().sm_count * kClipBlocksPerSm *
+         sizeof(double);
 }
 
 int grad_norm_clip(int64_t count, const int *dtypes, const void *const *grads, void *const *outs,
@@ -100,15 +321,20 @@ int grad_norm_clip(int64_t count, const int *dtypes, const void *const *grads, v
     return GEMM_ERR_INVALID_ARG;
   if (count > 0 && (!dtypes || !grads || !sizes)) return GEMM_ERR_INVALID_ARG;
   if (outs && !(max_norm >= 0.0f)) return GEMM_ERR_INVALID_ARG;
+  int64_t total = 0;
   for (int64_t i = 0; i < count; ++i) {
-    if (!dtype_known(dtypes[i]) || sizes[i] < 0 || sizes[i] > ((int64_t)1 << 46))
+    if (!dtype_known(dtypes[i]) || sizes[i] < 0 || sizes[i] > ((int64_t)1 << 40))
       return GEMM_ERR_INVALID_ARG;
     const uintptr_t mask = dtype_size(dtypes[i]) - 1;
     if (sizes[i] > 0 && (!grads[i] || (reinterpret_cast<uintptr_t>(grads[i]) & mask)))
       return GEMM_ERR_INVALID_ARG;
     if (outs && sizes[i] > 0 && (!outs[i] || (reinterpret_cast<uintptr_t>(outs[i]) & mask)))
       return GEMM_ERR_INVALID_ARG;
+    total += sizes[i];
   }
+  // 2^40 elements are more than any device's memory holds, and the chunks of
+  // fewer count in 32 bits
+  if (total > ((int64_t)1 << 40)) return GEMM_ERR_UNSUPPORTED;
   int dev = -1;
   int st = current_device(&dev);
   if (st != GEMM_OK) return st;
@@ -119,28 +345,9 @@ int grad_norm_clip(int64_t count, const int *dtypes, const void *const *grads, v
     st = library_workspace(dev, (size_t)need, &ws);
     if (st != GEMM_OK) return st;
   }
-  double *partial = static_cast<double *>(ws);
-  static thread_local ClipTable tab;
-  cudaError_t e = cudaSuccess;
-  for (int pass = 0; pass < (outs ? 2 : 1) && e == cudaSuccess; ++pass) {
-    for (int64_t at = 0; at < count && e == cudaSuccess; at += kClipTable) {
-      tab.count = (int)(count - at < kClipTable ? count - at : kClipTable);
-      for (int k = 0; k < tab.count; ++k)
-        tab.t[k] = {grads[at + k], outs ? outs[at + k] : nullptr, sizes[at + k], dtypes[at + k]};
-      if (pass == 0)
-        clip_sum_kernel<<<kClipBlocks, kClipThreads, 0, stream>>>(
-            tab, partial + at / kClipTable * kClipBlocks);
-      else
-        clip_scale_kernel<<<kClipBlocks, kClipThreads, 0, stream>>>(tab, norm, max_norm);
-      e = cudaGetLastError();
-    }
-    if (pass == 0 && e == cudaSuccess) {
-      clip_norm_kernel<<<1, kClipThreads, 0, stream>>>(partial, clip_launches(count) * kClipBlocks,
-                                                       norm);
-      e = cudaGetLastError();
-    }
-  }
-  return to_status(e);
+  const ClipCall q{count,    dtypes, grads, outs, sizes, props_of(dev).sm_count * kClipBlocksPerSm,
+                   static_cast<double *>(ws), max_norm, norm, stream};
+  return to_status(count <= kClipSmall ? clip_run<kClipSmall>(q) : clip_run<kClipTable>(q));
 }
 
 }  // extern "C"

@@ -6,11 +6,14 @@
 // each thread copies the codes that it alone will use to shared memory ahead
 // of time, asynchronously and a ring of stages deep, and the arithmetic per
 // code is kept under what that leaves: a 32-bit word of eight codes becomes
-// four pairs of BF16 by 3 shifts, 4 three-input logic operations (mask, and
-// or in the exponent of 128: 128 + q is exact) and 4 paired subtractions of
-// 136, which leave q - 8, exact too.  Scales multiply the FP32 sums of one
-// group; a zero point z other than 8 adds s (8 - z) sum x, with the sums of x
-// from one more MMA whose weights are ones.
+// four BF16 pairs 128 + q, exact, by 3 shifts and 4 three-input logic
+// operations that mask and or in the exponent of 128.  The ALU pipe, which
+// runs these at half the issue rate, is what the kernel is nearest to.
+// Scales multiply the FP32 sums of one group, from which (128 + z) sum x is
+// taken first, with the sums of x from MMAs whose weights are ones; that
+// difference costs about 5 of FP32's 24 bits, which a BF16 result does not
+// show.  With FP32 X the pairs are made q - 8 instead (exact, one paired
+// subtraction each) and only (z - 8) sum x is taken off.
 //
 // An MMA sums 16 values of k in any order, so a thread's eight codes of one
 // word are the k that it feeds to two MMAs, and X is loaded to match.  All k
@@ -19,6 +22,11 @@
 //
 // FP32 X is split into three BF16 (24 bits) that take three columns of an MMA
 // each token, so a tile holds 2 tokens, and 8 in BF16.
+//
+// A CTA has one block of rows and its warps split k; their sums meet in shared
+// memory in a fixed order.
+#include <cstdlib>
+
 #include "ff.cuh"
 
 namespace gg {
@@ -35,13 +43,11 @@ struct Q4Args {
   const void *x;
   void *y;
   Q4Side w[2];
-  int rows, blocks;  // weight rows of one block (of each matrix), blocks
-  int vec_x;         // rows of X start on 16-byte boundaries
+  int group_shift;  // group = 1 << group_shift
+  int vec_x;        // rows of X start on 16-byte boundaries
 };
 
-constexpr int kQ4Threads = 256, kQ4Warps = kQ4Threads / 32;
-constexpr int kTiles = 4;              // 16-row tiles of a warp (gated: two of each matrix)
-constexpr int kStageWords = 20480;     // shared memory of the code ring: 160 KB at W = 4
+constexpr int kMaxWarps = 16;  // of a CTA: its parts of k
 
 __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, int bytes) {
   if (bytes == 16)
@@ -68,10 +74,22 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes i and i + 4 of a word, as the BF16 pair (q - 8, q - 8).
-template <int I>
+// The same from a sum of zero.
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                uint32_t a2, uint32_t a3, uint32_t b0,
+                                                uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// Codes i and i + 4 of a word as the BF16 pair 128 + q or (EXACT) q - 8.
+template <bool EXACT, int I>
 __device__ __forceinline__ uint32_t codes(uint32_t w) {
   const uint32_t u = ((w >> (4 * I)) & 0x000f000fu) | 0x43004300u;
+  if (!EXACT) return u;
   __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162 *>(&u);
   h = __hsub2(h, __nv_bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308)));
   return *reinterpret_cast<uint32_t *>(&h);
@@ -90,21 +108,6 @@ template <typename T>
 struct Raw8 {
   uint4 v[sizeof(T) / 2];
 };
-
-template <typename T>
-__device__ __forceinline__ void load_x(Raw8<T> &r, const T *row, int64_t k, int64_t K, bool vec) {
-  if (vec && k + 8 <= K) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      r.v[i] = __ldg(reinterpret_cast<const uint4 *>(row + k) + i);
-  } else {
-    __align__(16) T t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = k + i < K ? row[k + i] : from_f32<T>(0.0f);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const uint4 *>(t)[i];
-  }
-}
 
 // The pairs (x_i, x_i+4), i = 0..3, of plane `plane`.
 __device__ __forceinline__ void pairs(const Raw8<bf16> &r, int, uint32_t (&b)[4]) {
@@ -131,287 +134,350 @@ __device__ __forceinline__ void pairs(const Raw8<float> &r, int plane, uint32_t 
   for (int i = 0; i < 4; ++i) b[i] = plane_of(f[i], plane) | (plane_of(f[i + 4], plane) << 16);
 }
 
-// W: words of codes of a thread, row and step.  NT: tiles of columns.  VEC:
-// every row of codes starts on a boundary of 4 W bytes; otherwise the aligned
-// words around a thread's bytes are copied, one more, and shifted when used.
-template <typename T, int W, int NT, bool GATED, bool VEC>
-__global__ void __launch_bounds__(kQ4Threads, 1) q4_kernel(const Q4Args p) {
-  constexpr int WW = VEC ? W : W + 1;
-  constexpr int STEP = 32 * W;                           // k of one step
-  constexpr int SLOT = kTiles * 2 * WW * kQ4Threads;     // words of one stage
-  constexpr int STAGES = kStageWords * 2 / SLOT > 10 ? 10 : kStageWords * 2 / SLOT;
-  constexpr int COLS = NT * 8;
-  constexpr int SIDE_TILES = GATED ? kTiles / 2 : kTiles;
-  extern __shared__ __align__(16) uint32_t ring[];
-  float *red = reinterpret_cast<float *>(ring + STAGES * SLOT);  // [warp][tile row][column]
+// W: words of codes of a thread, row and step.  TI: 16-row tiles of a warp
+// (gated: half of each matrix).  NT: tiles of columns.  VEC: every row of codes
+// starts on a boundary of 4 W bytes; otherwise the aligned words around a
+// thread's bytes are copied, one more, and shifted when used.
+template <typename T, int W, int TI, int NT, bool GATED, bool VEC>
+struct Q4Cfg {
+  static constexpr int WW = VEC ? W : W + 1;
+  static constexpr int STEP = 32 * W;                 // k of one step
+  static constexpr int SLOT = TI * 2 * WW;            // words of a stage for each thread
+  // warps that an SM holds, by registers: 24 with two tiles, 16 with four
+  static constexpr int SM_WARPS = TI == 4 ? 16 : 24;
+  static constexpr int DEEP = 227 * 1024 / (SM_WARPS * 128) / SLOT;
+  static constexpr int STAGES = DEEP > 8 ? 8 : DEEP;
+  static_assert(STAGES >= 2, "");
+  static constexpr int COLS = NT * 8;
+  static constexpr int TILES = GATED ? TI / 2 : TI;   // of one matrix
+  static constexpr int ROWS = TILES * 16;
+  static_assert(!GATED || TI % 2 == 0, "");
+  // the ring of a thread, or its warp's share of the sums
+  static constexpr int RING = STAGES * SLOT * 32, RED = TI * 16 * COLS;
+  static constexpr int WARP_BYTES = (RING > RED ? RING : RED) * 4;
+};
+
+template <typename T, int W, int TI, int NT, bool GATED, bool VEC>
+__global__ void __launch_bounds__(Q4Cfg<T, W, TI, NT, GATED, VEC>::SM_WARPS * 32, 1)
+q4_kernel(const Q4Args p) {
+  using Cfg = Q4Cfg<T, W, TI, NT, GATED, VEC>;
+  constexpr int WW = Cfg::WW, STEP = Cfg::STEP, SLOT = Cfg::SLOT, STAGES = Cfg::STAGES;
+  constexpr int COLS = Cfg::COLS, TILES = Cfg::TILES, SIDES = GATED ? 2 : 1;
+  constexpr bool EXACT = sizeof(T) == 4;
+  extern __shared__ __align__(16) uint32_t shared[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int warps = blockDim.x >> 5;
+  // this thread's ring: word w of a slot at ring[w * 32], or 4 W bytes together
+  uint32_t *ring = shared + warp * (Cfg::WARP_BYTES / 4) + (VEC ? lane * W : lane);
+  const bool has_z = p.w[0].z != nullptr;
   const int64_t m0 = (int64_t)blockIdx.y * (kTileTokens<T> * NT);
+  const int64_t n0 = (int64_t)blockIdx.x * Cfg::ROWS;
+  const int left = (int)(p.N - n0 < Cfg::ROWS ? p.N - n0 : Cfg::ROWS);
   const int steps = (int)((p.K + STEP - 1) / STEP);
-  const int mine = steps > warp ? (steps - warp + kQ4Warps - 1) / kQ4Warps : 0;
+  const int mine = steps > warp ? (steps - warp + warps - 1) / warps : 0;
   const int64_t row_bytes = (p.K + 1) / 2;
 
-  // The codes of this thread in step `c` of block `blk`, to slot `st`.
-  auto copy = [&](int blk, int c, int st) {
-    const int64_t n0 = (int64_t)blk * p.rows;
-    const int left = (int)(p.N - n0 < p.rows ? p.N - n0 : p.rows);
+  // Weight rows of the halves of the tiles.  Rows that the matrix does not
+  // have stand for its last one: what is computed of them is not stored.
+  uint32_t row[TILES][2];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const Q4Side &w = p.w[GATED && i >= SIDE_TILES];
-      const uint8_t *end = w.q + (p.N - 1) * w.ldq + row_bytes;
+  for (int i = 0; i < TILES; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = (i % SIDE_TILES) * 16 + 8 * h + g;
-        uint32_t *dst = ring + st * SLOT + (i * 2 + h) * WW * kQ4Threads;
-        if ((i % SIDE_TILES) * 16 >= left) continue;  // the whole tile: never read
-        const uint8_t *src = w.q + (n0 + r) * w.ldq + (int64_t)c * (STEP / 2) + t * (4 * W);
-        if constexpr (VEC) {
-          dst += tid * W;
-          if (r < left && src + 4 * W <= end) {
-            cp_async((uint32_t)__cvta_generic_to_shared(dst), src, 4 * W);
-            continue;
-          }
-        } else {
-          src -= reinterpret_cast<uintptr_t>(src) & 3;
-          if (r < left && src >= w.q && src + 4 * WW <= end) {
+    for (int h = 0; h < 2; ++h) {
+      const int r = i * 16 + 8 * h + g;
+      row[i][h] = (uint32_t)(r < left ? r : left - 1);
+    }
+  const uint8_t *base[SIDES];
+  const T *sbase[SIDES], *zbase[SIDES];
 #pragma unroll
-            for (int j = 0; j < WW; ++j)
-              cp_async((uint32_t)__cvta_generic_to_shared(dst + j * kQ4Threads + tid), src + 4 * j,
-                       4);
-            continue;
+  for (int k = 0; k < SIDES; ++k) {
+    base[k] = p.w[k].q + n0 * p.w[k].ldq + t * (4 * W);
+    sbase[k] = static_cast<const T *>(p.w[k].s) + n0 * p.groups;
+    zbase[k] = static_cast<const T *>(p.w[k].z) + (has_z ? n0 * p.groups : 0);
+  }
+
+  // The codes of this thread in step `c`, to slot `st`.
+  auto copy = [&](int c, int st) {
+    const int64_t at = (int64_t)c * (STEP / 2);
+    // A step inside the rows is copied as it is.  Words copied for unaligned
+    // rows begin and end in other rows, of which the matrix's ends have none.
+    bool inside = at + STEP / 2 <= row_bytes;
+    if (!VEC && ((n0 == 0 && c == 0) || (n0 + left == p.N && c + 2 >= steps))) inside = false;
+    uint32_t *slot = ring + st * (SLOT * 32);
+    auto each = [&](auto f) {
+#pragma unroll
+      for (int k = 0; k < SIDES; ++k)
+#pragma unroll
+        for (int i = 0; i < TILES; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t *src = base[k] + at + (uint64_t)row[i][h] * (uint32_t)p.w[k].ldq;
+            if (!VEC) src -= reinterpret_cast<uintptr_t>(src) & 3;
+            f(src, slot + ((k * TILES + i) * 2 + h) * WW * 32, k);
           }
-        }
-        // at the ends of the matrix byte by byte; code 8 where there is none
-        for (int j = 0; j < WW; ++j) {
-          uint32_t v = r < left ? 0 : 0x88888888u;
-          for (int b = 0; b < 4 && r < left; ++b) {
-            const uint8_t *at = src + 4 * j + b;
-            v |= (uint32_t)(at >= w.q && at < end ? *at : 0x88) << (8 * b);
-          }
-          dst[VEC ? j : j * kQ4Threads + tid] = v;
-        }
+    };
+    auto issue = [&](const uint8_t *src, uint32_t *dst) {
+      const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+      if constexpr (VEC) {
+        cp_async(to, src, 4 * W);
+      } else {
+#pragma unroll
+        for (int j = 0; j < WW; ++j) cp_async(to + j * 128, src + 4 * j, 4);
       }
+    };
+    if (inside) {
+      each([&](const uint8_t *src, uint32_t *dst, int) { issue(src, dst); });
+    } else {
+      each([&](const uint8_t *src, uint32_t *dst, int k) {
+        const uint8_t *first = p.w[k].q, *end = first + (p.N - 1) * p.w[k].ldq + row_bytes;
+        if (src >= first && src + 4 * WW <= end) {
+          issue(src, dst);
+          return;
+        }
+        // at the ends of the matrix: code 8 beyond it
+#pragma unroll 1
+        for (int j = 0; j < WW; ++j, src += 4) {
+          uint32_t v = 0x88888888u;
+          if (src >= first && src + 4 <= end) {
+            v = *reinterpret_cast<const uint32_t *>(src);
+          } else if (src < end && src + 4 > first) {
+            v = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              v |= (uint32_t)(src + b >= first && src + b < end ? src[b] : 0x88) << (8 * b);
+          }
+          dst[VEC ? j : j * 32] = v;
+        }
+      });
     }
   };
 
-  // This lane's column of each tile of X^T
-  const int col_token = column_token<T>(g), plane = sizeof(T) == 4 ? g % 3 : 0;
+  // This lane's column of each tile of X^T.  A column without a token stands
+  // for another one; its sums are not stored.
+  const int plane = sizeof(T) == 4 ? g % 3 : 0;
   const T *xrow[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int64_t m = m0 + nt * kTileTokens<T> + col_token;
-    xrow[nt] = col_token < kTileTokens<T> && m < p.M ? static_cast<const T *>(p.x) + m * p.ldx
-                                                     : nullptr;
+    const int64_t m = m0 + nt * kTileTokens<T> + column_token<T>(g);
+    xrow[nt] = static_cast<const T *>(p.x) + (m < p.M ? m : p.M - 1) * p.ldx + t * (8 * W);
   }
-  auto fetch_x = [&](int c, Raw8<T> (&r)[NT][W]) {
+  // The scales are loaded a step ahead, x at the step's start
+  Raw8<T> raw[NT][W];
+  T sraw[SIDES][TILES][2], zraw[SIDES][TILES][2];
+  auto fetch_x = [&](int c) {
+    const int64_t k0 = (int64_t)c * STEP;
+    if (p.vec_x != 0 && k0 + STEP <= p.K) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+          for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            raw[nt][j].v[i] =
+                __ldg(reinterpret_cast<const uint4 *>(xrow[nt] + k0) + j * (sizeof(T) / 2) + i);
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const int64_t n = p.K - k0 - t * (8 * W) - 8 * j;
+          __align__(16) T v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = i < n ? xrow[nt][k0 + 8 * j + i] : from_f32<T>(0.0f);
+#pragma unroll
+          for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            raw[nt][j].v[i] = reinterpret_cast<const uint4 *>(v)[i];
+        }
+    }
+  };
+  auto fetch_s = [&](int c) {
+    const int64_t grp = (int64_t)c * STEP >> p.group_shift;
+#pragma unroll
+    for (int k = 0; k < SIDES; ++k)
+#pragma unroll
+      for (int i = 0; i < TILES; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t at = (uint64_t)row[i][h] * (uint32_t)p.groups;
+          sraw[k][i][h] = (sbase[k] + grp)[at];
+          if (has_z) zraw[k][i][h] = (zbase[k] + grp)[at];
+        }
+  };
+
+#pragma unroll
+  for (int st = 0; st < STAGES - 1; ++st) {
+    if (st < mine) copy(warp + st * warps, st);
+    cp_async_commit();
+  }
+  float acc[TI][NT][4];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        if (xrow[nt] != nullptr) {
-          load_x(r[nt][j], xrow[nt], (int64_t)c * STEP + t * (8 * W) + 8 * j, p.K, p.vec_x != 0);
-        } else {
-#pragma unroll
-          for (int i = 0; i < (int)sizeof(T) / 2; ++i) r[nt][j].v[i] = make_uint4(0, 0, 0, 0);
-        }
-      }
-  };
-
-  // The copies run ahead of the arithmetic, over the ends of blocks too.
-  int cb = blockIdx.x, ci = 0;  // block and own step to copy next
-  auto copy_next = [&](int st) {
-    if (cb < p.blocks && mine > 0) {
-      copy(cb, warp + ci * kQ4Warps, st);
-      if (++ci == mine) {
-        ci = 0;
-        cb += gridDim.x;
-      }
-    }
-    cp_async_commit();
-  };
-#pragma unroll 1
-  for (int st = 0; st < STAGES - 1; ++st) copy_next(st);
+      for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
+  if (mine > 0) fetch_s(warp);
 
   int st = 0;
-  for (int blk = blockIdx.x; blk < p.blocks; blk += gridDim.x) {
-    const int64_t n0 = (int64_t)blk * p.rows;
-    const int left = (int)(p.N - n0 < p.rows ? p.N - n0 : p.rows);
-    float acc[kTiles][NT][4];
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
-
-    // x and the scales are loaded a step ahead
-    Raw8<T> raw[NT][W];
-    T sraw[kTiles][2], zraw[kTiles][2];
-    auto fetch_s = [&](int c) {
-      const int64_t grp = (int64_t)c * STEP / p.group;
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        const Q4Side &w = p.w[GATED && i >= SIDE_TILES];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = (i % SIDE_TILES) * 16 + 8 * h + g;
-          const int64_t at = (n0 + r) * p.groups + grp;
-          sraw[i][h] = r < left ? static_cast<const T *>(w.s)[at] : from_f32<T>(0.0f);
-          zraw[i][h] = r < left && w.z ? static_cast<const T *>(w.z)[at] : from_f32<T>(8.0f);
-        }
-      }
-    };
-    if (mine > 0) {
-      fetch_x(warp, raw);
-      fetch_s(warp);
-    }
 #pragma unroll 1
-    for (int it = 0; it < mine; ++it) {
-      const int c = warp + it * kQ4Warps;
-      float s[kTiles][2], z[kTiles][2];  // scales; 8 less the zero points
+  for (int it = 0; it < mine; ++it) {
+    const int c = warp + it * warps;
+    fetch_x(c);
+    uint32_t b[NT][W][4];
+    float s[TI][2], z[TI][2];  // scales; what is taken off of each code still
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
+    for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s[i][h] = to_f32(sraw[i][h]);
-          z[i][h] = 8.0f - to_f32(zraw[i][h]);
-        }
-      uint32_t b[NT][W][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < W; ++j) pairs(raw[nt][j], plane, b[nt][j]);
-      if (it + 1 < mine) {
-        fetch_x(c + kQ4Warps, raw);
-        fetch_s(c + kQ4Warps);
+      for (int h = 0; h < 2; ++h) {
+        s[i][h] = to_f32(sraw[i / TILES][i % TILES][h]);
+        z[i][h] = (EXACT ? 8.0f : -128.0f) - (has_z ? to_f32(zraw[i / TILES][i % TILES][h]) : 8.0f);
       }
-
-      cp_async_wait<STAGES - 2>();  // this step's codes are here (each thread reads its own)
-      const uint32_t *slot = ring + st * SLOT;
-      float xs[NT][4];
-      if (p.w[0].z != nullptr) {
+    if (it + 1 < mine) fetch_s(c + warps);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          xs[nt][0] = xs[nt][1] = xs[nt][2] = xs[nt][3] = 0.0f;
-          constexpr uint32_t one = 0x3f803f80u;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
-            mma_16816(xs[nt], one, one, one, one, b[nt][j][0], b[nt][j][1]);
-            mma_16816(xs[nt], one, one, one, one, b[nt][j][2], b[nt][j][3]);
-          }
-        }
-      }
+      for (int j = 0; j < W; ++j) pairs(raw[nt][j], plane, b[nt][j]);
+    float xs[NT][4];
+    if (!EXACT || has_z) {
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        if ((i % SIDE_TILES) * 16 >= left) continue;
-        uint32_t w[2][W];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t *src = slot + (i * 2 + h) * WW * kQ4Threads;
-          if constexpr (VEC) {
-            src += tid * W;
-            if constexpr (W == 4)
-              *reinterpret_cast<uint4 *>(w[h]) = *reinterpret_cast<const uint4 *>(src);
-            else if constexpr (W == 2)
-              *reinterpret_cast<uint2 *>(w[h]) = *reinterpret_cast<const uint2 *>(src);
-            else
-              w[h][0] = src[0];
-          } else {
-            const Q4Side &sd = p.w[GATED && i >= SIDE_TILES];
-            const int r = (i % SIDE_TILES) * 16 + 8 * h + g;
-            const int shift = 8 * (int)((reinterpret_cast<uintptr_t>(sd.q) + (n0 + r) * sd.ldq) & 3);
-            uint32_t lo = src[tid];
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-              const uint32_t hi = src[(j + 1) * kQ4Threads + tid];
-              w[h][j] = __funnelshift_r(lo, hi, shift);
-              lo = hi;
-            }
-          }
-        }
-        float d[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.0f;
+      for (int nt = 0; nt < NT; ++nt) {
+        constexpr uint32_t one = 0x3f803f80u;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-          const uint32_t a0 = codes<0>(w[0][j]), a1 = codes<0>(w[1][j]), a2 = codes<1>(w[0][j]),
-                         a3 = codes<1>(w[1][j]), a4 = codes<2>(w[0][j]), a5 = codes<2>(w[1][j]),
-                         a6 = codes<3>(w[0][j]), a7 = codes<3>(w[1][j]);
+          if (j == 0)
+            mma_16816_first(xs[nt], one, one, one, one, b[nt][j][0], b[nt][j][1]);
+          else
+            mma_16816(xs[nt], one, one, one, one, b[nt][j][0], b[nt][j][1]);
+          mma_16816(xs[nt], one, one, one, one, b[nt][j][2], b[nt][j][3]);
+        }
+      }
+    }
+    cp_async_wait<STAGES - 2>();  // this step's codes are here (each thread reads its own)
+    const uint32_t *slot = ring + st * (SLOT * 32);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_16816(d[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
-            mma_16816(d[nt], a4, a5, a6, a7, b[nt][j][2], b[nt][j][3]);
+    for (int i = 0; i < TI; ++i) {
+      uint32_t w[2][W];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t *src = slot + (i * 2 + h) * WW * 32;
+        if constexpr (VEC) {
+          if constexpr (W == 4)
+            *reinterpret_cast<uint4 *>(w[h]) = *reinterpret_cast<const uint4 *>(src);
+          else if constexpr (W == 2)
+            *reinterpret_cast<uint2 *>(w[h]) = *reinterpret_cast<const uint2 *>(src);
+          else
+            w[h][0] = src[0];
+        } else {
+          const Q4Side &sd = p.w[i / TILES];
+          const int shift = 8 * (((uint32_t)reinterpret_cast<uintptr_t>(base[i / TILES]) +
+                                  row[i % TILES][h] * (uint32_t)sd.ldq) & 3);
+          uint32_t lo = src[0];
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            const uint32_t hi = src[(j + 1) * 32];
+            w[h][j] = __funnelshift_r(lo, hi, shift);
+            lo = hi;
           }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = d[nt][e];
-            if (p.w[0].z != nullptr) v = fmaf(z[i][e >> 1], xs[nt][e], v);
-            acc[i][nt][e] = fmaf(s[i][e >> 1], v, acc[i][nt][e]);
-          }
       }
-      copy_next(st == 0 ? STAGES - 1 : st - 1);  // the slot that the step before freed
-      if (++st == STAGES) st = 0;
-    }
-
-    // The warps' sums over their steps, added in order; then, FP32, the planes.
+      float d[NT][4];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i)
+      for (int j = 0; j < W; ++j) {
+        const uint32_t a0 = codes<EXACT, 0>(w[0][j]), a1 = codes<EXACT, 0>(w[1][j]),
+                       a2 = codes<EXACT, 1>(w[0][j]), a3 = codes<EXACT, 1>(w[1][j]),
+                       a4 = codes<EXACT, 2>(w[0][j]), a5 = codes<EXACT, 2>(w[1][j]),
+                       a6 = codes<EXACT, 3>(w[0][j]), a7 = codes<EXACT, 3>(w[1][j]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (j == 0)
+            mma_16816_first(d[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
+          else
+            mma_16816(d[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
+          mma_16816(d[nt], a4, a5, a6, a7, b[nt][j][2], b[nt][j][3]);
+        }
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2 *>(red + ((warp * kTiles + i) * 16 + 8 * h + g) * COLS + nt * 8 +
-                                      2 * t) =
-              make_float2(acc[i][nt][2 * h], acc[i][nt][2 * h + 1]);
-    __syncthreads();
-    constexpr int ROWS = SIDE_TILES * 16, TOKENS = kTileTokens<T> * NT;
-    auto total = [&](int row, int m) {
-      float v = 0.0f;
-      constexpr int PLANES = sizeof(T) == 4 ? 3 : 1;
-      const int col = m / kTileTokens<T> * 8 + m % kTileTokens<T> * PLANES;
-#pragma unroll
-      for (int q = PLANES - 1; q >= 0; --q)
-#pragma unroll
-        for (int w = 0; w < kQ4Warps; ++w)
-          v += red[(w * kTiles * 16 + row) * COLS + col + q];
-      return v;
-    };
-    for (int e = tid; e < ROWS * TOKENS; e += kQ4Threads) {
-      const int r = e % ROWS, m = e / ROWS;
-      if (r >= left || m0 + m >= p.M) continue;
-      float y = total(r, m);
-      if constexpr (GATED) {
-        const float u = total(ROWS + r, m);
-        with_act(p.act, [&](auto a) { y = act_of<sizeof(T) == 2, decltype(a)::value>(y) * u; });
-      }
-      static_cast<T *>(p.y)[(m0 + m) * p.ldy + n0 + r] = from_f32<T>(y);
+        for (int e = 0; e < 4; ++e) {
+          float v = d[nt][e];
+          if (!EXACT || has_z) v = fmaf(z[i][e >> 1], xs[nt][e], v);
+          acc[i][nt][e] = fmaf(s[i][e >> 1], v, acc[i][nt][e]);
+        }
     }
-    __syncthreads();  // red is written again
+    // the slot that the step before freed
+    if (it + STAGES - 1 < mine) copy(c + (STAGES - 1) * warps, st == 0 ? STAGES - 1 : st - 1);
+    cp_async_commit();
+    if (++st == STAGES) st = 0;
   }
+
+  // The warps' sums, added in order; then, FP32, the planes.  They take the
+  // place of the rings, which every warp has emptied.
   cp_async_wait<0>();
+  __syncthreads();
+  float *red = reinterpret_cast<float *>(shared);  // [warp][tile row][column]
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2 *>(red + ((warp * TI + i) * 16 + 8 * h + g) * COLS + nt * 8 +
+                                    2 * t) = make_float2(acc[i][nt][2 * h], acc[i][nt][2 * h + 1]);
+  __syncthreads();
+  constexpr int TOKENS = kTileTokens<T> * NT;
+  auto total = [&](int r, int m) {
+    float v = 0.0f;
+    constexpr int PLANES = sizeof(T) == 4 ? 3 : 1;
+    const int col = m / kTileTokens<T> * 8 + m % kTileTokens<T> * PLANES;
+#pragma unroll
+    for (int q = PLANES - 1; q >= 0; --q)
+#pragma unroll 4
+      for (int w = 0; w < warps; ++w) v += red[(w * TI * 16 + r) * COLS + col + q];
+    return v;
+  };
+  const int tokens = (int)(p.M - m0 < TOKENS ? p.M - m0 : TOKENS);
+  for (int e = tid; e < Cfg::ROWS * tokens; e += blockDim.x) {
+    const int r = e % Cfg::ROWS, m = e / Cfg::ROWS;
+    if (r >= left) continue;
+    float y = total(r, m);
+    if constexpr (GATED) {
+      const float u = total(Cfg::ROWS + r, m);
+      with_act(p.act, [&](auto a) { y = act_of<sizeof(T) == 2, decltype(a)::value>(y) * u; });
+    }
+    static_cast<T *>(p.y)[(m0 + m) * p.ldy + n0 + r] = from_f32<T>(y);
+  }
 }
 
-template <typename T, int W, int NT, bool GATED, bool VEC>
-cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, int sms) {
-  constexpr int SLOT = kTiles * 2 * (VEC ? W : W + 1) * kQ4Threads;
-  constexpr int STAGES = kStageWords * 2 / SLOT > 10 ? 10 : kStageWords * 2 / SLOT;
-  constexpr int smem = (STAGES * SLOT + kQ4Warps * kTiles * 16 * NT * 8) * 4;
-  static_assert(smem <= 227 * 1024 && STAGES >= 3, "");
-  auto kern = q4_kernel<T, W, NT, GATED, VEC>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename T, int W, int TI, int NT, bool GATED, bool VEC>
+cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, int warps) {
+  using Cfg = Q4Cfg<T, W, TI, NT, GATED, VEC>;
+  static_assert(Cfg::WARP_BYTES * kMaxWarps <= 227 * 1024, "");
+  auto kern = q4_kernel<T, W, TI, NT, GATED, VEC>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cfg::WARP_BYTES * kMaxWarps);
   if (e != cudaSuccess) return e;
-  const int64_t ty = ceil_div(p.M, kTileTokens<T> * NT);
-  kern<<<dim3((unsigned)(p.blocks < sms ? p.blocks : sms), (unsigned)ty), kQ4Threads, smem, s>>>(p);
+  kern<<<dim3((unsigned)ceil_div(p.N, Cfg::ROWS), (unsigned)ceil_div(p.M, kTileTokens<T> * NT)),
+         warps * 32, Cfg::WARP_BYTES * warps, s>>>(p);
   return cudaGetLastError();
 }
 
+// Tiles and warps: two tiles for one tile of columns, so that six CTAs of four
+// warps share an SM; four tiles for two, whose x is then loaded half as often.
 template <typename T, int W, bool GATED, bool VEC>
-cudaError_t pick_nt(const Q4Args &p, cudaStream_t s, int sms) {
-  return p.M <= kTileTokens<T> ? launch_q4<T, W, 1, GATED, VEC>(p, s, sms)
-                               : launch_q4<T, W, 2, GATED, VEC>(p, s, sms);
+cudaError_t pick_tiles(const Q4Args &p, cudaStream_t s, int sms) {
+  const int steps = (int)ceil_div(p.K, 32 * W);
+  const bool wide = p.M > kTileTokens<T>;
+  const int tiles = wide ? 4 : 2;
+  const int64_t ctas = ceil_div(p.N, tiles * 16 / (GATED ? 2 : 1));
+  const int most = wide ? 16 : 24;  // warps that an SM holds
+  int warps = (int)(most * sms / ctas);
+  warps = warps < 4 ? 4 : warps > kMaxWarps ? kMaxWarps : warps;
+  if (warps > steps) warps = steps < 1 ? 1 : steps;
+  if (const char *e = std::getenv("Q4_WARPS")) warps = std::atoi(e);
+  return wide ? launch_q4<T, W, 4, 2, GATED, VEC>(p, s, warps)
+              : launch_q4<T, W, 2, 1, GATED, VEC>(p, s, warps);
 }
 
 template <typename T, int W, bool GATED>
@@ -419,8 +485,8 @@ cudaError_t pick_vec(const Q4Args &p, cudaStream_t s, int sms) {
   uintptr_t bits = 0;
   for (int k = 0; k < (GATED ? 2 : 1); ++k)
     bits |= reinterpret_cast<uintptr_t>(p.w[k].q) | (p.N > 1 ? (uintptr_t)p.w[k].ldq : 0);
-  return bits % (4 * W) == 0 ? pick_nt<T, W, GATED, true>(p, s, sms)
-                             : pick_nt<T, W, GATED, false>(p, s, sms);
+  return bits % (4 * W) == 0 ? pick_tiles<T, W, GATED, true>(p, s, sms)
+                             : pick_tiles<T, W, GATED, false>(p, s, sms);
 }
 
 template <typename T, bool GATED>
@@ -432,7 +498,7 @@ cudaError_t pick_group(const Q4Args &p, cudaStream_t s, int sms) {
 
 bool side_ok(const Q4Side &w, const Q4Args &p, int dtype) {
   const uintptr_t mask = dtype_size(dtype) - 1;
-  if (w.ldq < (p.K + 1) / 2) return false;
+  if (w.ldq < (p.K + 1) / 2 || w.ldq >= ((int64_t)1 << 32)) return false;
   if (p.M == 0 || p.N == 0 || p.K == 0) return true;
   return w.q && w.s && !(reinterpret_cast<uintptr_t>(w.s) & mask) &&
          !(reinterpret_cast<uintptr_t>(w.z) & mask);
@@ -458,11 +524,8 @@ int run_q4(int dtype, int sides, Q4Args p, cudaStream_t stream) {
   int dev = -1;
   const int st = current_device(&dev);
   if (st != GEMM_OK) return st;
-  // Blocks of equal rows, as many for each SM, at most what a warp's tiles hold.
   const int sms = props_of(dev).sm_count;
-  const int64_t most = kTiles * 16 / sides, rounds = ceil_div(p.N, most * sms);
-  p.rows = (int)ceil_div(p.N, rounds * sms);
-  p.blocks = (int)ceil_div(p.N, p.rows);
+  p.group_shift = p.group == 32 ? 5 : p.group == 64 ? 6 : p.group == 128 ? 7 : 8;
   p.vec_x = ((reinterpret_cast<uintptr_t>(p.x) | (p.M > 1 ? (uintptr_t)p.ldx * size : 0)) & 15) == 0;
   cudaError_t e;
   if (dtype == GEMM_DT_F32)
