@@ -4,9 +4,12 @@
 // Two kernels: the sum of squares, and the scaling, which adds the blocks'
 // sums in a fixed order first.  Both are bound by HBM: every gradient is read
 // twice (a set larger than L2 cannot wait on the chip for the norm) and
-// written once.  The tensors are cut into chunks of 16 KB; a block takes a
-// run of neighbouring chunks, in the second kernel backwards, so that it
-// begins with what the first one left in L2.
+// written once.  The tensors are cut into chunks of 32 KB, eight 16-byte loads
+// in flight a thread, which the blocks take in turn: first to last in the
+// first kernel and last to first in the second, so that it begins with what
+// the first one left in L2.  600 M gradients (1.32 GB) on GB300: 626 us, 6.3
+// TB/s over the three passes; with chunks of 16 KB 688, with a run of
+// neighbouring chunks for each block 637.
 #include "ff.cuh"
 #include "tc_common.cuh"
 
@@ -27,7 +30,7 @@ struct ClipTable {
   ClipTensor t[N];
 };
 constexpr int kClipSmall = 64, kClipTable = 1000;  // tensors of one launch
-constexpr int kClipThreads = 256, kClipVectors = 4;
+constexpr int kClipThreads = 256, kClipVectors = 8;
 constexpr int kClipChunk = kClipThreads * kClipVectors;  // 16-byte vectors of a chunk
 constexpr int kClipBlocksPerSm = 8;
 
@@ -135,11 +138,9 @@ template <int N>
 __global__ void __launch_bounds__(kClipThreads)
 clip_sum_kernel(const __grid_constant__ ClipTable<N> tab, double *partial) {
   tc::grid_dependency_wait();
-  const int c0 = (int)((int64_t)tab.chunks * blockIdx.x / gridDim.x);
-  const int c1 = (int)((int64_t)tab.chunks * (blockIdx.x + 1) / gridDim.x);
   double sum = 0.0;
-  int k = clip_find(tab, c0);
-  for (int c = c0; c < c1; ++c) {
+  int k = clip_find(tab, blockIdx.x);
+  for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
     while (k + 1 < tab.count && tab.t[k + 1].first <= c) ++k;
     const ClipTensor &t = tab.t[k];
     const int64_t v0 = (int64_t)(c - t.first) * kClipChunk;
@@ -210,10 +211,10 @@ clip_scale_kernel(const __grid_constant__ ClipTable<N> tab, const double *partia
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
   const float r = max_norm / (n + 1e-6f);
   const float s = r < 1.0f || r != r ? r : 1.0f;
-  const int c0 = (int)((int64_t)tab.chunks * blockIdx.x / gridDim.x);
-  const int c1 = (int)((int64_t)tab.chunks * (blockIdx.x + 1) / gridDim.x);
-  int k = c1 > c0 ? clip_find(tab, c1 - 1) : 0;
-  for (int c = c1 - 1; c >= c0; --c) {
+  // the grid is no larger than the number of chunks
+  const int last = blockIdx.x + (tab.chunks - 1 - blockIdx.x) / gridDim.x * gridDim.x;
+  int k = clip_find(tab, last);
+  for (int c = last; c >= 0; c -= gridDim.x) {
     while (tab.t[k].first > c) --k;
     const ClipTensor &t = tab.t[k];
     if (s == 1.0f && t.in == t.out) continue;  // x * 1 is there already
