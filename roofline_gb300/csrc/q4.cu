@@ -45,6 +45,7 @@ struct Q4Args {
   Q4Side w[2];
   int group_shift;  // group = 1 << group_shift
   int vec_x;        // rows of X start on 16-byte boundaries
+  int aligned, scales_aligned;  // rows of codes on 16 bytes; a step's scales on theirs
 };
 
 constexpr int kMaxWarps = 16;  // of a CTA: its parts of k
@@ -134,122 +135,136 @@ __device__ __forceinline__ void pairs(const Raw8<float> &r, int plane, uint32_t 
   for (int i = 0; i < 4; ++i) b[i] = plane_of(f[i], plane) | (plane_of(f[i + 4], plane) << 16);
 }
 
-// W: words of codes of a thread, row and step.  TI: 16-row tiles of a warp
-// (gated: half of each matrix).  NT: tiles of columns.  VEC: every row of codes
-// starts on a boundary of 4 W bytes; otherwise the aligned words around a
-// thread's bytes are copied, one more, and shifted when used.
-template <typename T, int W, int TI, int NT, bool GATED, bool VEC>
+// W: words of codes that a thread takes of a row and group (a group is 32 W
+// values of k, or twice that).  TI: 16-row tiles of a warp (gated: half of
+// each matrix).  NT: tiles of columns.
+template <typename T, int W, int TI, int NT, bool GATED>
 struct Q4Cfg {
-  static constexpr int WW = VEC ? W : W + 1;
-  static constexpr int STEP = 32 * W;                 // k of one step
-  static constexpr int SLOT = TI * 2 * WW;            // words of a stage for each thread
-  // warps that an SM holds, by registers: 24 with two tiles, 16 with four
-  static constexpr int SM_WARPS = TI == 4 ? 16 : 24;
-  static constexpr int DEEP = 227 * 1024 / (SM_WARPS * 128) / SLOT;
-  static constexpr int STAGES = DEEP > 8 ? 8 : DEEP;
-  static_assert(STAGES >= 2, "");
+  static constexpr int STEP = 256;                  // k of one step: 128 bytes of codes a row
+  static constexpr int PARTS = STEP / (32 * W);     // groups of a step
   static constexpr int COLS = NT * 8;
-  static constexpr int TILES = GATED ? TI / 2 : TI;   // of one matrix
+  static constexpr int TILES = GATED ? TI / 2 : TI; // of one matrix
   static constexpr int ROWS = TILES * 16;
+  static constexpr int STAGES = 2;
+  static constexpr int SCALES = TI * 16 * PARTS * (int)sizeof(T);  // bytes, one stage
+  static constexpr int SLOT = TI * 16 * 128 + 2 * SCALES;          // codes, scales, zero points
   static_assert(!GATED || TI % 2 == 0, "");
-  // the ring of a thread, or its warp's share of the sums
-  static constexpr int RING = STAGES * SLOT * 32, RED = TI * 16 * COLS;
-  static constexpr int WARP_BYTES = (RING > RED ? RING : RED) * 4;
+  // the ring of a warp, or its share of the sums
+  static constexpr int RING = STAGES * SLOT, RED = TI * 16 * COLS * 4;
+  static constexpr int WARP_BYTES = RING > RED ? RING : RED;
+  // warps that an SM holds
+  static constexpr int BY_SMEM = 226 * 1024 / WARP_BYTES, BY_REGS = TI == 4 ? 12 : 24;
+  static constexpr int SM_WARPS = BY_SMEM < BY_REGS ? BY_SMEM / 4 * 4 : BY_REGS;
+  static constexpr int MAX_WARPS = SM_WARPS < kMaxWarps ? SM_WARPS : kMaxWarps;
 };
 
-template <typename T, int W, int TI, int NT, bool GATED, bool VEC>
-__global__ void __launch_bounds__(Q4Cfg<T, W, TI, NT, GATED, VEC>::SM_WARPS * 32, 1)
+template <typename T, int W, int TI, int NT, bool GATED>
+__global__ void __launch_bounds__(Q4Cfg<T, W, TI, NT, GATED>::SM_WARPS * 32, 1)
 q4_kernel(const Q4Args p) {
-  using Cfg = Q4Cfg<T, W, TI, NT, GATED, VEC>;
-  constexpr int WW = Cfg::WW, STEP = Cfg::STEP, SLOT = Cfg::SLOT, STAGES = Cfg::STAGES;
-  constexpr int COLS = Cfg::COLS, TILES = Cfg::TILES, SIDES = GATED ? 2 : 1;
+  using Cfg = Q4Cfg<T, W, TI, NT, GATED>;
+  constexpr int STEP = Cfg::STEP, PARTS = Cfg::PARTS, STAGES = Cfg::STAGES, RW = TI * 16;
+  constexpr int COLS = Cfg::COLS, TILES = Cfg::TILES, ROWS = Cfg::ROWS;
   constexpr bool EXACT = sizeof(T) == 4;
-  extern __shared__ __align__(16) uint32_t shared[];
+  extern __shared__ __align__(128) uint8_t shared[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warps = blockDim.x >> 5;
-  // this thread's ring: word w of a slot at ring[w * 32], or 4 W bytes together
-  uint32_t *ring = shared + warp * (Cfg::WARP_BYTES / 4) + (VEC ? lane * W : lane);
+  uint8_t *ring = shared + warp * Cfg::WARP_BYTES;
   const bool has_z = p.w[0].z != nullptr;
   const int64_t m0 = (int64_t)blockIdx.y * (kTileTokens<T> * NT);
-  const int64_t n0 = (int64_t)blockIdx.x * Cfg::ROWS;
-  const int left = (int)(p.N - n0 < Cfg::ROWS ? p.N - n0 : Cfg::ROWS);
+  const int64_t n0 = (int64_t)blockIdx.x * ROWS;
+  const int left = (int)(p.N - n0 < ROWS ? p.N - n0 : ROWS);
   const int steps = (int)((p.K + STEP - 1) / STEP);
   const int mine = steps > warp ? (steps - warp + warps - 1) / warps : 0;
   const int64_t row_bytes = (p.K + 1) / 2;
+  // Rows that the matrix does not have stand for its last one: what is
+  // computed of them is not stored.
+  auto weight_row = [&](int r) { return n0 + (r < left ? r : left - 1); };
 
-  // Weight rows of the halves of the tiles.  Rows that the matrix does not
-  // have stand for its last one: what is computed of them is not stored.
-  uint32_t row[TILES][2];
-#pragma unroll
-  for (int i = 0; i < TILES; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = i * 16 + 8 * h + g;
-      row[i][h] = (uint32_t)(r < left ? r : left - 1);
-    }
-  const uint8_t *base[SIDES];
-  const T *sbase[SIDES], *zbase[SIDES];
-#pragma unroll
-  for (int k = 0; k < SIDES; ++k) {
-    base[k] = p.w[k].q + n0 * p.w[k].ldq + t * (4 * W);
-    sbase[k] = static_cast<const T *>(p.w[k].s) + n0 * p.groups;
-    zbase[k] = static_cast<const T *>(p.w[k].z) + (has_z ? n0 * p.groups : 0);
-  }
+  // Row r's 16-byte piece c, placed so that the four threads of a row and its
+  // neighbours meet every bank once, whether they read 4, 8 or 16 bytes each.
+  auto piece = [](int r, int c) {
+    return r * 128 + ((c ^ ((r & 1) << 2 | (r & 2) | ((r >> 2) & 1))) * 16);
+  };
 
-  // The codes of this thread in step `c`, to slot `st`.
+  // Where this lane's copies begin: 16 bytes of every fourth row.
+  const int lr = lane >> 3, lc = lane & 7;
+  const uint8_t *from[GATED ? 2 : 1];
+#pragma unroll
+  for (int k = 0; k < (GATED ? 2 : 1); ++k) from[k] = p.w[k].q + n0 * p.w[k].ldq + lc * 16;
+  const int to[2] = {piece(lr, lc), piece(4 + lr, lc) - 512};
+
+  // Step `c`'s codes, scales and zero points of all the warp's rows, to slot `st`.
   auto copy = [&](int c, int st) {
+    uint8_t *slot = ring + st * Cfg::SLOT;
     const int64_t at = (int64_t)c * (STEP / 2);
-    // A step inside the rows is copied as it is.  Words copied for unaligned
-    // rows begin and end in other rows, of which the matrix's ends have none.
-    bool inside = at + STEP / 2 <= row_bytes;
-    if (!VEC && ((n0 == 0 && c == 0) || (n0 + left == p.N && c + 2 >= steps))) inside = false;
-    uint32_t *slot = ring + st * (SLOT * 32);
-    auto each = [&](auto f) {
-#pragma unroll
-      for (int k = 0; k < SIDES; ++k)
-#pragma unroll
-        for (int i = 0; i < TILES; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint8_t *src = base[k] + at + (uint64_t)row[i][h] * (uint32_t)p.w[k].ldq;
-            if (!VEC) src -= reinterpret_cast<uintptr_t>(src) & 3;
-            f(src, slot + ((k * TILES + i) * 2 + h) * WW * 32, k);
-          }
+    auto source = [&](int i) {  // of rows 4 i on
+      const int k = i * 4 / ROWS, r = i * 4 % ROWS + lr;
+      return from[k] + at + (uint64_t)(uint32_t)(r < left ? r : left - 1) * (uint32_t)p.w[k].ldq;
     };
-    auto issue = [&](const uint8_t *src, uint32_t *dst) {
-      const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
-      if constexpr (VEC) {
-        cp_async(to, src, 4 * W);
-      } else {
+    if (p.aligned && at + STEP / 2 <= row_bytes) {
+      const uint32_t dst = (uint32_t)__cvta_generic_to_shared(slot);
 #pragma unroll
-        for (int j = 0; j < WW; ++j) cp_async(to + j * 128, src + 4 * j, 4);
-      }
-    };
-    if (inside) {
-      each([&](const uint8_t *src, uint32_t *dst, int) { issue(src, dst); });
+      for (int i = 0; i < RW / 4; ++i) cp_async(dst + to[i & 1] + i * 512, source(i), 16);
     } else {
-      each([&](const uint8_t *src, uint32_t *dst, int k) {
-        const uint8_t *first = p.w[k].q, *end = first + (p.N - 1) * p.w[k].ldq + row_bytes;
-        if (src >= first && src + 4 * WW <= end) {
-          issue(src, dst);
-          return;
-        }
-        // at the ends of the matrix: code 8 beyond it
+      // unaligned rows, and the ends of the rows: the aligned words that hold
+      // the piece, shifted; code 8 beyond the matrix
 #pragma unroll 1
-        for (int j = 0; j < WW; ++j, src += 4) {
-          uint32_t v = 0x88888888u;
-          if (src >= first && src + 4 <= end) {
-            v = *reinterpret_cast<const uint32_t *>(src);
-          } else if (src < end && src + 4 > first) {
-            v = 0;
+      for (int i = 0; i < RW / 4; ++i) {
+        const uint8_t *src = source(i);
+        const Q4Side &w = p.w[i * 4 / ROWS];
+        const uint8_t *first = w.q, *end = first + (p.N - 1) * w.ldq + row_bytes;
+        const int off = (int)(reinterpret_cast<uintptr_t>(src) & 3);
+        src -= off;
+        uint32_t v[5];
+        if (src >= first && src + 20 <= end) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-              v |= (uint32_t)(src + b >= first && src + b < end ? src[b] : 0x88) << (8 * b);
+          for (int j = 0; j < 5; ++j) v[j] = __ldg(reinterpret_cast<const uint32_t *>(src) + j);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 5; ++j) {
+            v[j] = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const uint8_t *q = src + 4 * j + b;
+              v[j] |= (uint32_t)(q >= first && q < end ? *q : 0x88) << (8 * b);
+            }
           }
-          dst[VEC ? j : j * 32] = v;
         }
-      });
+        *reinterpret_cast<uint4 *>(slot + (i & 1 ? to[1] : to[0]) + i * 512) =
+            make_uint4(__funnelshift_r(v[0], v[1], 8 * off), __funnelshift_r(v[1], v[2], 8 * off),
+                       __funnelshift_r(v[2], v[3], 8 * off), __funnelshift_r(v[3], v[4], 8 * off));
+      }
+    }
+    // scales and zero points: PARTS a row, in the order of k
+    const int64_t grp = ((int64_t)c * STEP) >> p.group_shift;
+    T *ds = reinterpret_cast<T *>(slot + RW * 128);
+    constexpr int BYTES = PARTS * (int)sizeof(T), PIECE = BYTES < 16 ? BYTES : 16;
+    constexpr int PER = BYTES / PIECE;  // pieces of a row
+    if (p.scales_aligned && grp + PARTS <= p.groups) {
+#pragma unroll
+      for (int i = 0; i < RW * PER / 32; ++i) {
+        const int e = i * 32 + lane, r = e / PER, k = r / ROWS, o = e % PER * (PIECE / (int)sizeof(T));
+        const Q4Side &w = p.w[GATED ? k : 0];
+        const int64_t from = weight_row(r - k * ROWS) * p.groups + grp + o;
+        T *dst = ds + r * PARTS + o;
+        cp_async((uint32_t)__cvta_generic_to_shared(dst), static_cast<const T *>(w.s) + from, PIECE);
+        if (has_z)
+          cp_async((uint32_t)__cvta_generic_to_shared(dst + RW * PARTS),
+                   static_cast<const T *>(w.z) + from, PIECE);
+      }
+    } else {
+#pragma unroll 1
+      for (int e = lane; e < RW * PARTS; e += 32) {
+        const int r = e / PARTS, k = r / ROWS;
+        const Q4Side &w = p.w[GATED ? k : 0];
+        const int64_t gr = ((int64_t)c * STEP + e % PARTS * (32 * W)) >> p.group_shift;
+        const int64_t from = weight_row(r - k * ROWS) * p.groups + gr;
+        ds[e] = gr < p.groups ? static_cast<const T *>(w.s)[from] : from_f32<T>(0.0f);
+        if (has_z)
+          ds[RW * PARTS + e] = gr < p.groups ? static_cast<const T *>(w.z)[from]
+                                             : from_f32<T>(0.0f);
+      }
     }
   };
 
@@ -262,12 +277,10 @@ q4_kernel(const Q4Args p) {
     const int64_t m = m0 + nt * kTileTokens<T> + column_token<T>(g);
     xrow[nt] = static_cast<const T *>(p.x) + (m < p.M ? m : p.M - 1) * p.ldx + t * (8 * W);
   }
-  // The scales are loaded a step ahead, x at the step's start
-  Raw8<T> raw[NT][W];
-  T sraw[SIDES][TILES][2], zraw[SIDES][TILES][2];
-  auto fetch_x = [&](int c) {
-    const int64_t k0 = (int64_t)c * STEP;
-    if (p.vec_x != 0 && k0 + STEP <= p.K) {
+  // The x of the group that begins at k0, as the MMAs' B operands
+  auto fetch_x = [&](int64_t k0, uint32_t (&b)[NT][W][4]) {
+    Raw8<T> raw[NT][W];
+    if (p.vec_x != 0 && k0 + 32 * W <= p.K) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -290,22 +303,13 @@ q4_kernel(const Q4Args p) {
             raw[nt][j].v[i] = reinterpret_cast<const uint4 *>(v)[i];
         }
     }
-  };
-  auto fetch_s = [&](int c) {
-    const int64_t grp = (int64_t)c * STEP >> p.group_shift;
 #pragma unroll
-    for (int k = 0; k < SIDES; ++k)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < TILES; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint64_t at = (uint64_t)row[i][h] * (uint32_t)p.groups;
-          sraw[k][i][h] = (sbase[k] + grp)[at];
-          if (has_z) zraw[k][i][h] = (zbase[k] + grp)[at];
-        }
+      for (int j = 0; j < W; ++j) pairs(raw[nt][j], plane, b[nt][j]);
   };
 
-#pragma unroll
+#pragma unroll 1
   for (int st = 0; st < STAGES - 1; ++st) {
     if (st < mine) copy(warp + st * warps, st);
     cp_async_commit();
@@ -317,99 +321,78 @@ q4_kernel(const Q4Args p) {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
-  if (mine > 0) fetch_s(warp);
 
-  int st = 0;
 #pragma unroll 1
   for (int it = 0; it < mine; ++it) {
-    const int c = warp + it * warps;
-    fetch_x(c);
-    uint32_t b[NT][W][4];
-    float s[TI][2], z[TI][2];  // scales; what is taken off of each code still
+    const int c = warp + it * warps, st = it % STAGES;
+    cp_async_wait<STAGES - 2>();
+    __syncwarp();  // this step is here, and every lane is done with the one before
+    if (it + STAGES - 1 < mine) copy(c + (STAGES - 1) * warps, (it + STAGES - 1) % STAGES);
+    cp_async_commit();
+    const uint8_t *slot = ring + st * Cfg::SLOT;
+    const T *ds = reinterpret_cast<const T *>(slot + RW * 128);
+#pragma unroll 1
+    for (int part = 0; part < PARTS; ++part) {
+      uint32_t b[NT][W][4];
+      fetch_x((int64_t)c * STEP + part * (32 * W), b);
+      float xs[NT][4];
+      if (!EXACT || has_z) {
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+        for (int nt = 0; nt < NT; ++nt) {
+          constexpr uint32_t one = 0x3f803f80u;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        s[i][h] = to_f32(sraw[i / TILES][i % TILES][h]);
-        z[i][h] = (EXACT ? 8.0f : -128.0f) - (has_z ? to_f32(zraw[i / TILES][i % TILES][h]) : 8.0f);
-      }
-    if (it + 1 < mine) fetch_s(c + warps);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < W; ++j) pairs(raw[nt][j], plane, b[nt][j]);
-    float xs[NT][4];
-    if (!EXACT || has_z) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        constexpr uint32_t one = 0x3f803f80u;
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          if (j == 0)
-            mma_16816_first(xs[nt], one, one, one, one, b[nt][j][0], b[nt][j][1]);
-          else
-            mma_16816(xs[nt], one, one, one, one, b[nt][j][0], b[nt][j][1]);
-          mma_16816(xs[nt], one, one, one, one, b[nt][j][2], b[nt][j][3]);
+          for (int j = 0; j < W; ++j) {
+            if (j == 0)
+              mma_16816_first(xs[nt], one, one, one, one, b[nt][j][0], b[nt][j][1]);
+            else
+              mma_16816(xs[nt], one, one, one, one, b[nt][j][0], b[nt][j][1]);
+            mma_16816(xs[nt], one, one, one, one, b[nt][j][2], b[nt][j][3]);
+          }
         }
       }
-    }
-    cp_async_wait<STAGES - 2>();  // this step's codes are here (each thread reads its own)
-    const uint32_t *slot = ring + st * (SLOT * 32);
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      uint32_t w[2][W];
+      for (int i = 0; i < TI; ++i) {
+        uint32_t w[2][W];
+        float s[2], z[2];  // scales; what is taken off of each code still
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t *src = slot + (i * 2 + h) * WW * 32;
-        if constexpr (VEC) {
+        for (int h = 0; h < 2; ++h) {
+          const int r = i * 16 + 8 * h + g;
+          const uint8_t *src = slot + piece(r, (part * 4 * W + t * W) / 4) + t * W % 4 * 4;
           if constexpr (W == 4)
             *reinterpret_cast<uint4 *>(w[h]) = *reinterpret_cast<const uint4 *>(src);
           else if constexpr (W == 2)
             *reinterpret_cast<uint2 *>(w[h]) = *reinterpret_cast<const uint2 *>(src);
           else
-            w[h][0] = src[0];
-        } else {
-          const Q4Side &sd = p.w[i / TILES];
-          const int shift = 8 * (((uint32_t)reinterpret_cast<uintptr_t>(base[i / TILES]) +
-                                  row[i % TILES][h] * (uint32_t)sd.ldq) & 3);
-          uint32_t lo = src[0];
+            w[h][0] = *reinterpret_cast<const uint32_t *>(src);
+          s[h] = to_f32(ds[r * PARTS + part]);
+          z[h] = (EXACT ? 8.0f : -128.0f) - (has_z ? to_f32(ds[(RW + r) * PARTS + part]) : 8.0f);
+        }
+        float d[NT][4];
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
-            const uint32_t hi = src[(j + 1) * 32];
-            w[h][j] = __funnelshift_r(lo, hi, shift);
-            lo = hi;
+        for (int j = 0; j < W; ++j) {
+          const uint32_t a0 = codes<EXACT, 0>(w[0][j]), a1 = codes<EXACT, 0>(w[1][j]),
+                         a2 = codes<EXACT, 1>(w[0][j]), a3 = codes<EXACT, 1>(w[1][j]),
+                         a4 = codes<EXACT, 2>(w[0][j]), a5 = codes<EXACT, 2>(w[1][j]),
+                         a6 = codes<EXACT, 3>(w[0][j]), a7 = codes<EXACT, 3>(w[1][j]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (j == 0)
+              mma_16816_first(d[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
+            else
+              mma_16816(d[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
+            mma_16816(d[nt], a4, a5, a6, a7, b[nt][j][2], b[nt][j][3]);
           }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = d[nt][e];
+            if (!EXACT || has_z) v = fmaf(z[e >> 1], xs[nt][e], v);
+            acc[i][nt][e] = fmaf(s[e >> 1], v, acc[i][nt][e]);
+          }
       }
-      float d[NT][4];
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        const uint32_t a0 = codes<EXACT, 0>(w[0][j]), a1 = codes<EXACT, 0>(w[1][j]),
-                       a2 = codes<EXACT, 1>(w[0][j]), a3 = codes<EXACT, 1>(w[1][j]),
-                       a4 = codes<EXACT, 2>(w[0][j]), a5 = codes<EXACT, 2>(w[1][j]),
-                       a6 = codes<EXACT, 3>(w[0][j]), a7 = codes<EXACT, 3>(w[1][j]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (j == 0)
-            mma_16816_first(d[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
-          else
-            mma_16816(d[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
-          mma_16816(d[nt], a4, a5, a6, a7, b[nt][j][2], b[nt][j][3]);
-        }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = d[nt][e];
-          if (!EXACT || has_z) v = fmaf(z[i][e >> 1], xs[nt][e], v);
-          acc[i][nt][e] = fmaf(s[i][e >> 1], v, acc[i][nt][e]);
-        }
     }
-    // the slot that the step before freed
-    if (it + STAGES - 1 < mine) copy(c + (STAGES - 1) * warps, st == 0 ? STAGES - 1 : st - 1);
-    cp_async_commit();
-    if (++st == STAGES) st = 0;
   }
 
   // The warps' sums, added in order; then, FP32, the planes.  They take the
@@ -434,66 +417,62 @@ q4_kernel(const Q4Args p) {
 #pragma unroll
     for (int q = PLANES - 1; q >= 0; --q)
 #pragma unroll 4
-      for (int w = 0; w < warps; ++w) v += red[(w * TI * 16 + r) * COLS + col + q];
+      for (int w = 0; w < warps; ++w) v += red[(w * RW + r) * COLS + col + q];
     return v;
   };
   const int tokens = (int)(p.M - m0 < TOKENS ? p.M - m0 : TOKENS);
-  for (int e = tid; e < Cfg::ROWS * tokens; e += blockDim.x) {
-    const int r = e % Cfg::ROWS, m = e / Cfg::ROWS;
+  for (int e = tid; e < ROWS * tokens; e += blockDim.x) {
+    const int r = e % ROWS, m = e / ROWS;
     if (r >= left) continue;
     float y = total(r, m);
     if constexpr (GATED) {
-      const float u = total(Cfg::ROWS + r, m);
+      const float u = total(ROWS + r, m);
       with_act(p.act, [&](auto a) { y = act_of<sizeof(T) == 2, decltype(a)::value>(y) * u; });
     }
     static_cast<T *>(p.y)[(m0 + m) * p.ldy + n0 + r] = from_f32<T>(y);
   }
 }
 
-template <typename T, int W, int TI, int NT, bool GATED, bool VEC>
-cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, int warps) {
-  using Cfg = Q4Cfg<T, W, TI, NT, GATED, VEC>;
-  static_assert(Cfg::WARP_BYTES * kMaxWarps <= 227 * 1024, "");
-  auto kern = q4_kernel<T, W, TI, NT, GATED, VEC>;
+template <typename T, int W, int TI, int NT, bool GATED>
+cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, int sms) {
+  using Cfg = Q4Cfg<T, W, TI, NT, GATED>;
+  static_assert(Cfg::WARP_BYTES * Cfg::MAX_WARPS <= 227 * 1024 && Cfg::MAX_WARPS >= 4, "");
+  auto kern = q4_kernel<T, W, TI, NT, GATED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg::WARP_BYTES * kMaxWarps);
+                                       Cfg::WARP_BYTES * Cfg::MAX_WARPS);
   if (e != cudaSuccess) return e;
-  kern<<<dim3((unsigned)ceil_div(p.N, Cfg::ROWS), (unsigned)ceil_div(p.M, kTileTokens<T> * NT)),
-         warps * 32, Cfg::WARP_BYTES * warps, s>>>(p);
+  // Warps: as many as fill the SMs, but no more than there are steps.
+  const int64_t ctas = ceil_div(p.N, Cfg::ROWS), steps = ceil_div(p.K, Cfg::STEP);
+  int64_t warps = (int64_t)Cfg::SM_WARPS * sms / ctas;
+  warps = warps < 4 ? 4 : warps > Cfg::MAX_WARPS ? Cfg::MAX_WARPS : warps;
+  if (warps > steps) warps = steps < 1 ? 1 : steps;
+  if (const char *e = std::getenv("Q4_WARPS")) warps = std::atoi(e) < Cfg::MAX_WARPS ? std::atoi(e) : Cfg::MAX_WARPS;
+  kern<<<dim3((unsigned)ctas, (unsigned)ceil_div(p.M, kTileTokens<T> * NT)), (unsigned)warps * 32,
+         Cfg::WARP_BYTES * warps, s>>>(p);
   return cudaGetLastError();
 }
 
-// Tiles and warps: two tiles for one tile of columns, so that six CTAs of four
-// warps share an SM; four tiles for two, whose x is then loaded half as often.
-template <typename T, int W, bool GATED, bool VEC>
-cudaError_t pick_tiles(const Q4Args &p, cudaStream_t s, int sms) {
-  const int steps = (int)ceil_div(p.K, 32 * W);
-  const bool wide = p.M > kTileTokens<T>;
-  const int tiles = wide ? 4 : 2;
-  const int64_t ctas = ceil_div(p.N, tiles * 16 / (GATED ? 2 : 1));
-  const int most = wide ? 16 : 24;  // warps that an SM holds
-  int warps = (int)(most * sms / ctas);
-  warps = warps < 4 ? 4 : warps > kMaxWarps ? kMaxWarps : warps;
-  if (warps > steps) warps = steps < 1 ? 1 : steps;
-  if (const char *e = std::getenv("Q4_WARPS")) warps = std::atoi(e);
-  return wide ? launch_q4<T, W, 4, 2, GATED, VEC>(p, s, warps)
-              : launch_q4<T, W, 2, 1, GATED, VEC>(p, s, warps);
-}
-
+// Two tiles for one tile of columns; four for two, whose x is then loaded
+// half as often.
 template <typename T, int W, bool GATED>
-cudaError_t pick_vec(const Q4Args &p, cudaStream_t s, int sms) {
-  uintptr_t bits = 0;
-  for (int k = 0; k < (GATED ? 2 : 1); ++k)
-    bits |= reinterpret_cast<uintptr_t>(p.w[k].q) | (p.N > 1 ? (uintptr_t)p.w[k].ldq : 0);
-  return bits % (4 * W) == 0 ? pick_tiles<T, W, GATED, true>(p, s, sms)
-                             : pick_tiles<T, W, GATED, false>(p, s, sms);
+cudaError_t pick_tiles(Q4Args p, cudaStream_t s, int sms) {
+  constexpr int parts = 8 / W, bytes = parts * (int)sizeof(T) < 16 ? parts * (int)sizeof(T) : 16;
+  uintptr_t q = 0, sc = (uintptr_t)p.groups * sizeof(T);
+  for (int k = 0; k < (GATED ? 2 : 1); ++k) {
+    q |= reinterpret_cast<uintptr_t>(p.w[k].q) | (p.N > 1 ? (uintptr_t)p.w[k].ldq : 0);
+    sc |= reinterpret_cast<uintptr_t>(p.w[k].s) | reinterpret_cast<uintptr_t>(p.w[k].z);
+  }
+  p.aligned = q % 16 == 0;
+  p.scales_aligned = p.group == 32 * W && sc % bytes == 0 && bytes >= 4;
+  return p.M > kTileTokens<T> ? launch_q4<T, W, 4, 2, GATED>(p, s, sms)
+                              : launch_q4<T, W, 2, 1, GATED>(p, s, sms);
 }
 
 template <typename T, bool GATED>
 cudaError_t pick_group(const Q4Args &p, cudaStream_t s, int sms) {
-  return p.group == 32   ? pick_vec<T, 1, GATED>(p, s, sms)
-         : p.group == 64 ? pick_vec<T, 2, GATED>(p, s, sms)
-                         : pick_vec<T, 4, GATED>(p, s, sms);
+  return p.group == 32   ? pick_tiles<T, 1, GATED>(p, s, sms)
+         : p.group == 64 ? pick_tiles<T, 2, GATED>(p, s, sms)
+                         : pick_tiles<T, 4, GATED>(p, s, sms);
 }
 
 bool side_ok(const Q4Side &w, const Q4Args &p, int dtype) {
