@@ -43,6 +43,7 @@ struct Q4Args {
   const void *x;
   void *y;
   Q4Side w[2];
+  uint32_t mask;    // 0x000f000f
   int group_shift;  // group = 1 << group_shift
   int vec_x;        // rows of X start on 16-byte boundaries
   int aligned, scales_aligned;  // rows of codes on 16 bytes; a step's scales on theirs
@@ -87,9 +88,12 @@ __device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint
 }
 
 // Codes i and i + 4 of a word as the BF16 pair 128 + q or (EXACT) q - 8.
+// `mask` is 0x000f000f out of a register: mask and exponent as two immediates
+// would take two instructions.
 template <bool EXACT, int I>
-__device__ __forceinline__ uint32_t codes(uint32_t w) {
-  const uint32_t u = ((w >> (4 * I)) & 0x000f000fu) | 0x43004300u;
+__device__ __forceinline__ uint32_t codes(uint32_t w, uint32_t mask) {
+  uint32_t u;
+  asm("lop3.b32 %0, %1, %2, 0x43004300, 0xea;" : "=r"(u) : "r"(w >> (4 * I)), "r"(mask));
   if (!EXACT) return u;
   __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162 *>(&u);
   h = __hsub2(h, __nv_bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308)));
@@ -152,8 +156,9 @@ struct Q4Cfg {
   // the ring of a warp, or its share of the sums
   static constexpr int RING = STAGES * SLOT, RED = TI * 16 * COLS * 4;
   static constexpr int WARP_BYTES = RING > RED ? RING : RED;
-  // warps that an SM holds
-  static constexpr int BY_SMEM = 226 * 1024 / WARP_BYTES, BY_REGS = TI == 4 ? 12 : 24;
+  // Warps that an SM holds.  With four tiles 8 run faster than 12 (16 x 8192 x
+  // 28672: 68 against 78 us): what shared memory they leave is L1 for x.
+  static constexpr int BY_SMEM = 226 * 1024 / WARP_BYTES, BY_REGS = TI == 4 ? 8 : 16;
   static constexpr int SM_WARPS = BY_SMEM < BY_REGS ? BY_SMEM / 4 * 4 : BY_REGS;
   static constexpr int MAX_WARPS = SM_WARPS < kMaxWarps ? SM_WARPS : kMaxWarps;
 };
@@ -171,6 +176,7 @@ q4_kernel(const Q4Args p) {
   const int warps = blockDim.x >> 5;
   uint8_t *ring = shared + warp * Cfg::WARP_BYTES;
   const bool has_z = p.w[0].z != nullptr;
+  const uint32_t mask = p.mask;
   const int64_t m0 = (int64_t)blockIdx.y * (kTileTokens<T> * NT);
   const int64_t n0 = (int64_t)blockIdx.x * ROWS;
   const int left = (int)(p.N - n0 < ROWS ? p.N - n0 : ROWS);
@@ -277,9 +283,9 @@ q4_kernel(const Q4Args p) {
     const int64_t m = m0 + nt * kTileTokens<T> + column_token<T>(g);
     xrow[nt] = static_cast<const T *>(p.x) + (m < p.M ? m : p.M - 1) * p.ldx + t * (8 * W);
   }
-  // The x of the group that begins at k0, as the MMAs' B operands
-  auto fetch_x = [&](int64_t k0, uint32_t (&b)[NT][W][4]) {
-    Raw8<T> raw[NT][W];
+  // The x of the group that begins at k0: loaded a group ahead
+  Raw8<T> raw[NT][W];
+  auto fetch_x = [&](int64_t k0) {
     if (p.vec_x != 0 && k0 + 32 * W <= p.K) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -303,10 +309,6 @@ q4_kernel(const Q4Args p) {
             raw[nt][j].v[i] = reinterpret_cast<const uint4 *>(v)[i];
         }
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < W; ++j) pairs(raw[nt][j], plane, b[nt][j]);
   };
 
 #pragma unroll 1
@@ -322,6 +324,7 @@ q4_kernel(const Q4Args p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
 
+  if (mine > 0) fetch_x((int64_t)warp * STEP);
 #pragma unroll 1
   for (int it = 0; it < mine; ++it) {
     const int c = warp + it * warps, st = it % STAGES;
@@ -333,8 +336,15 @@ q4_kernel(const Q4Args p) {
     const T *ds = reinterpret_cast<const T *>(slot + RW * 128);
 #pragma unroll 1
     for (int part = 0; part < PARTS; ++part) {
-      uint32_t b[NT][W][4];
-      fetch_x((int64_t)c * STEP + part * (32 * W), b);
+      uint32_t b[NT][W][4];  // as the MMAs take it
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < W; ++j) pairs(raw[nt][j], plane, b[nt][j]);
+      if (part + 1 < PARTS)
+        fetch_x((int64_t)c * STEP + (part + 1) * (32 * W));
+      else if (it + 1 < mine)
+        fetch_x((int64_t)(c + warps) * STEP);
       float xs[NT][4];
       if (!EXACT || has_z) {
 #pragma unroll
@@ -370,10 +380,10 @@ q4_kernel(const Q4Args p) {
         float d[NT][4];
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-          const uint32_t a0 = codes<EXACT, 0>(w[0][j]), a1 = codes<EXACT, 0>(w[1][j]),
-                         a2 = codes<EXACT, 1>(w[0][j]), a3 = codes<EXACT, 1>(w[1][j]),
-                         a4 = codes<EXACT, 2>(w[0][j]), a5 = codes<EXACT, 2>(w[1][j]),
-                         a6 = codes<EXACT, 3>(w[0][j]), a7 = codes<EXACT, 3>(w[1][j]);
+          const uint32_t a0 = codes<EXACT, 0>(w[0][j], mask), a1 = codes<EXACT, 0>(w[1][j], mask),
+                         a2 = codes<EXACT, 1>(w[0][j], mask), a3 = codes<EXACT, 1>(w[1][j], mask),
+                         a4 = codes<EXACT, 2>(w[0][j], mask), a5 = codes<EXACT, 2>(w[1][j], mask),
+                         a6 = codes<EXACT, 3>(w[0][j], mask), a7 = codes<EXACT, 3>(w[1][j], mask);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if (j == 0)
@@ -504,6 +514,7 @@ int run_q4(int dtype, int sides, Q4Args p, cudaStream_t stream) {
   const int st = current_device(&dev);
   if (st != GEMM_OK) return st;
   const int sms = props_of(dev).sm_count;
+  p.mask = 0x000f000f;
   p.group_shift = p.group == 32 ? 5 : p.group == 64 ? 6 : p.group == 128 ? 7 : 8;
   p.vec_x = ((reinterpret_cast<uintptr_t>(p.x) | (p.M > 1 ? (uintptr_t)p.ldx * size : 0)) & 15) == 0;
   cudaError_t e;
