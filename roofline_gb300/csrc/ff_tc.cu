@@ -214,7 +214,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
 
 // What a warp's blocks of 32 rows x 16 columns become: c = v, or (gated)
 // act(v) * w with v and w themselves to g and u if given.
-template <typename T, bool GATED, bool FAST>
+template <typename T, bool GATED>
 struct Writer {
   uint8_t *st;  // the warp's 4 KB of shared memory: v, then w
   T *c;
@@ -234,7 +234,7 @@ struct Writer {
   __device__ __forceinline__ void combine(float (&x)[8], const float (&y)[8]) const {
     with_act(act, [&](auto a) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = act_of<FAST, decltype(a)::value>(x[i]) * y[i];
+      for (int i = 0; i < 8; ++i) x[i] = act_of<decltype(a)::value>(x[i]) * y[i];
     });
   }
 
@@ -518,7 +518,7 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
     auto aligned = [](const void *q, int64_t ld, int64_t size) {
       return ((reinterpret_cast<uintptr_t>(q) | (uintptr_t)(ld * size)) & 15) == 0;
     };
-    Writer<T, GATED, P == 1> out;
+    Writer<T, GATED> out;
     out.st = st;
     out.N = p.N;
     out.act = p.act;

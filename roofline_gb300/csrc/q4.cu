@@ -25,8 +25,6 @@
 //
 // A CTA has one block of rows and its warps split k; their sums meet in shared
 // memory in a fixed order.
-#include <cstdlib>
-
 #include "ff.cuh"
 
 namespace gg {
@@ -347,18 +345,17 @@ q4_kernel(const Q4Args p) {
         fetch_x((int64_t)(c + warps) * STEP);
       float xs[NT][4];
       if (!EXACT || has_z) {
+        constexpr uint32_t one = 0x3f803f80u;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          constexpr uint32_t one = 0x3f803f80u;
+        for (int j = 0; j < 2 * W; ++j)
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t b0 = b[nt][j / 2][j % 2 * 2], b1 = b[nt][j / 2][j % 2 * 2 + 1];
             if (j == 0)
-              mma_16816_first(xs[nt], one, one, one, one, b[nt][j][0], b[nt][j][1]);
+              mma_16816_first(xs[nt], one, one, one, one, b0, b1);
             else
-              mma_16816(xs[nt], one, one, one, one, b[nt][j][0], b[nt][j][1]);
-            mma_16816(xs[nt], one, one, one, one, b[nt][j][2], b[nt][j][3]);
+              mma_16816(xs[nt], one, one, one, one, b0, b1);
           }
-        }
       }
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
@@ -377,7 +374,9 @@ q4_kernel(const Q4Args p) {
           s[h] = to_f32(ds[r * PARTS + part]);
           z[h] = (EXACT ? 8.0f : -128.0f) - (has_z ? to_f32(ds[(RW + r) * PARTS + part]) : 8.0f);
         }
-        float d[NT][4];
+        // two sums a tile: an MMA that adds to the one before it waits 31 clocks
+        // for it, and one can begin every 9
+        float d[NT][4], d2[NT][4];
 #pragma unroll
         for (int j = 0; j < W; ++j) {
           const uint32_t a0 = codes<EXACT, 0>(w[0][j], mask), a1 = codes<EXACT, 0>(w[1][j], mask),
@@ -390,14 +389,20 @@ q4_kernel(const Q4Args p) {
               mma_16816_first(d[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
             else
               mma_16816(d[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
-            mma_16816(d[nt], a4, a5, a6, a7, b[nt][j][2], b[nt][j][3]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (j == 0)
+              mma_16816_first(d2[nt], a4, a5, a6, a7, b[nt][j][2], b[nt][j][3]);
+            else
+              mma_16816(d2[nt], a4, a5, a6, a7, b[nt][j][2], b[nt][j][3]);
           }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float v = d[nt][e];
+            float v = d[nt][e] + d2[nt][e];
             if (!EXACT || has_z) v = fmaf(z[e >> 1], xs[nt][e], v);
             acc[i][nt][e] = fmaf(s[e >> 1], v, acc[i][nt][e]);
           }
@@ -437,7 +442,7 @@ q4_kernel(const Q4Args p) {
     float y = total(r, m);
     if constexpr (GATED) {
       const float u = total(ROWS + r, m);
-      with_act(p.act, [&](auto a) { y = act_of<sizeof(T) == 2, decltype(a)::value>(y) * u; });
+      with_act(p.act, [&](auto a) { y = act_of<decltype(a)::value>(y) * u; });
     }
     static_cast<T *>(p.y)[(m0 + m) * p.ldy + n0 + r] = from_f32<T>(y);
   }
@@ -456,7 +461,6 @@ cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, int sms) {
   int64_t warps = (int64_t)Cfg::SM_WARPS * sms / ctas;
   warps = warps < 4 ? 4 : warps > Cfg::MAX_WARPS ? Cfg::MAX_WARPS : warps;
   if (warps > steps) warps = steps < 1 ? 1 : steps;
-  if (const char *e = std::getenv("Q4_WARPS")) warps = std::atoi(e) < Cfg::MAX_WARPS ? std::atoi(e) : Cfg::MAX_WARPS;
   kern<<<dim3((unsigned)ctas, (unsigned)ceil_div(p.M, kTileTokens<T> * NT)), (unsigned)warps * 32,
          Cfg::WARP_BYTES * warps, s>>>(p);
   return cudaGetLastError();

@@ -44,7 +44,7 @@ def _dtype(t) -> int:
 
 def _rows(t, name, rows, cols, dtype, device):
     """Leading dimension of a row-major rows x cols matrix."""
-    if t.shape != (rows, cols) or t.dtype != dtype or t.get_device() != device:
+    if t.shape != (rows, cols) or t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{name} must be {rows} x {cols}, {dtype}, on CUDA device {device}: got "
                          f"{tuple(t.shape)}, {t.dtype}, {t.device}")
     s0, s1 = t.stride()
@@ -56,17 +56,21 @@ def _rows(t, name, rows, cols, dtype, device):
 
 def _first(t, name):
     """(rows, cols, leading dimension, dtype code, device index) of the matrix that sets them."""
-    if not t.is_cuda or t.dim() != 2:
+    device = t.get_device()
+    if device < 0 or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     rows, cols = t.shape
-    device = t.get_device()
-    return rows, cols, _rows(t, name, rows, cols, t.dtype, device), _dtype(t), device
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    # the row stride of a one-row matrix is never used
+    return rows, cols, (s0 if rows > 1 else cols) or 1, _dtype(t), device
 
 
 def _weight(t, name, D, F, dtype, device):
     """{op: ld} of the ways a D x F weight can be read: row-major is op N,
     ``W.t()`` of a stored F x D matrix op T (one row or column may be either)."""
-    if t.shape != (D, F) or t.dtype != dtype or t.get_device() != device:
+    if t.shape != (D, F) or t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{name} must be {D} x {F}, {dtype}, on CUDA device {device}: got "
                          f"{tuple(t.shape)}, {t.dtype}, {t.device}")
     s0, s1 = t.stride()
@@ -188,22 +192,20 @@ def gated_ff_workspace(M, D, F, dtype, op_w=OP_N, backward=False, aligned=False)
     return out.value
 
 
-def _q4_side(q, s, z, dtype, device, K, group, name):
-    """(codes, ldq, scales, zero points) of one quantised matrix, checked against K and group."""
-    N, width = q.shape
-    if q.dtype != torch.uint8 or q.get_device() != device or width != (K + 1) // 2:
-        raise ValueError(f"{name} must be N x {(K + 1) // 2}, uint8, on CUDA device {device}")
+def _q4_side(q, s, z, N, K, groups, dtype, device, name):
+    """(ldq, address of the zero points) of one quantised matrix, checked."""
+    width = (K + 1) // 2
+    if q.shape != (N, width) or q.dtype is not torch.uint8 or q.get_device() != device:
+        raise ValueError(f"{name} must be {N} x {width}, uint8, on CUDA device {device}")
     ldq, one = q.stride()
     if one != 1 and width > 1:
         raise ValueError(f"{name} must have unit column stride")
-    shape = (N, -(-K // group))
-    for t, what in ((s, "scales"), (z, "zeros")):
-        if t is not None and (t.shape != shape or t.dtype != dtype or t.get_device() != device or
-                              not t.is_contiguous()):
-            raise ValueError(f"{what} of {name} must be {shape[0]} x {shape[1]}, contiguous, "
+    for t in (s,) if z is None else (s, z):
+        if (t.shape != (N, groups) or t.dtype is not dtype or t.get_device() != device or
+                not t.is_contiguous()):
+            raise ValueError(f"scales and zeros of {name} must be {N} x {groups}, contiguous, "
                              f"{dtype}, on CUDA device {device}")
-    return (q.data_ptr(), (ldq if N > 1 else width) or 1, s.data_ptr(),
-            None if z is None else z.data_ptr())
+    return (ldq if N > 1 else width) or 1, None if z is None else z.data_ptr()
 
 
 def q4_matmul(X, Wq, scales, zeros=None, group=128, out=None, stream=None):
@@ -214,11 +216,16 @@ def q4_matmul(X, Wq, scales, zeros=None, group=128, out=None, stream=None):
     if group <= 0 or Wq.dim() != 2:
         raise ValueError("group must be positive and Wq a 2-D tensor")
     N, dtype = Wq.shape[0], X.dtype
-    q, ldq, s, z = _q4_side(Wq, scales, zeros, dtype, dev, K, group, "Wq")
-    Y = torch.empty((M, N), dtype=dtype, device=X.device) if out is None else out
-    ldy = (N or 1) if out is None else _rows(out, "out", M, N, dtype, dev)
-    _check(_lib().q4_matmul(dt, M, N, K, X.data_ptr(), ldx, q, ldq, s, z, group, Y.data_ptr(), ldy,
-                            _stream(stream, dev, None if out is not None else Y)), "q4_matmul")
+    ldq, z = _q4_side(Wq, scales, zeros, N, K, -(-K // group), dtype, dev, "Wq")
+    if out is None:
+        Y, ldy = torch.empty((M, N), dtype=dtype, device=X.device), N or 1
+    else:
+        Y, ldy = out, _rows(out, "out", M, N, dtype, dev)
+    rc = _lib().q4_matmul(dt, M, N, K, X.data_ptr(), ldx, Wq.data_ptr(), ldq, scales.data_ptr(), z,
+                          group, Y.data_ptr(), ldy,
+                          _stream(stream, dev, None if out is not None else Y))
+    if rc:
+        _check(rc, "q4_matmul")
     return Y
 
 
@@ -226,17 +233,21 @@ def q4_gated(X, Wq_g, scales_g, Wq_u, scales_u, zeros_g=None, zeros_u=None, grou
              act="silu", out=None, stream=None):
     """H = act(X @ Wg.t()) * (X @ Wu.t()), both weights in the format of ``q4_matmul``."""
     M, K, ldx, dt, dev = _first(X, "X")
-    if group <= 0 or Wq_g.dim() != 2 or Wq_u.dim() != 2:
-        raise ValueError("group must be positive, Wq_g and Wq_u 2-D tensors")
-    N, dtype = Wq_g.shape[0], X.dtype
-    if Wq_u.shape[0] != N:
-        raise ValueError("Wq_g and Wq_u must have the same number of rows")
-    g = _q4_side(Wq_g, scales_g, zeros_g, dtype, dev, K, group, "Wq_g")
-    u = _q4_side(Wq_u, scales_u, zeros_u, dtype, dev, K, group, "Wq_u")
-    H = torch.empty((M, N), dtype=dtype, device=X.device) if out is None else out
-    ldh = (N or 1) if out is None else _rows(out, "out", M, N, dtype, dev)
-    _check(_lib().q4_gated(dt, _act(act), M, N, K, X.data_ptr(), ldx, *g, *u, group, H.data_ptr(),
-                           ldh, _stream(stream, dev, None if out is not None else H)), "q4_gated")
+    if group <= 0 or Wq_g.dim() != 2:
+        raise ValueError("group must be positive and Wq_g a 2-D tensor")
+    N, dtype, groups = Wq_g.shape[0], X.dtype, -(-K // group)
+    ldg, zg = _q4_side(Wq_g, scales_g, zeros_g, N, K, groups, dtype, dev, "Wq_g")
+    ldu, zu = _q4_side(Wq_u, scales_u, zeros_u, N, K, groups, dtype, dev, "Wq_u")
+    if out is None:
+        H, ldh = torch.empty((M, N), dtype=dtype, device=X.device), N or 1
+    else:
+        H, ldh = out, _rows(out, "out", M, N, dtype, dev)
+    rc = _lib().q4_gated(dt, _act(act), M, N, K, X.data_ptr(), ldx, Wq_g.data_ptr(), ldg,
+                         scales_g.data_ptr(), zg, Wq_u.data_ptr(), ldu, scales_u.data_ptr(), zu,
+                         group, H.data_ptr(), ldh,
+                         _stream(stream, dev, None if out is not None else H))
+    if rc:
+        _check(rc, "q4_gated")
     return H
 
 
