@@ -1,17 +1,22 @@
-"""Builds libgb300gemm.so in-tree with nvcc for sm_103a.
+"""Builds libgb300gemm.so in-tree with nvcc for sm_103a, and the torch binding
+of its feed-forward operators.
 
 Each .cu file in csrc/ is compiled to an object in parallel, then linked
-into one shared library (static CUDA runtime, no torch dependency).  Run
+into one shared library (static CUDA runtime, no torch dependency).
+torch_binding.cpp becomes the Python module _ff_native.so beside it, built
+with g++ against the installed torch's headers.  Run
 ``python -m roofline_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgb300gemm.so")
 INCLUDE = os.path.join(ROOT, "include")
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
+BINDING = os.path.join(BUILD, "_ff_native.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -37,14 +44,14 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return _sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
@@ -59,20 +66,54 @@ def _compile(src: str, log_dir: str) -> str:
     return obj
 
 
+def _compile_binding(log_dir: str) -> str:
+    """torch_binding.cpp to an object (its link needs the library)."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(BUILD, "torch_binding.o")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           "-Wall", "-I", INCLUDE, "-isystem", os.path.join(torch_dir, "include"), "-isystem",
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-isystem",
+           sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    with open(os.path.join(log_dir, "torch_binding.cpp.txt"), "w") as f:
+        f.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stderr[-4000:]}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, "-L",
+           os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-L", BUILD, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libgb300gemm.so if any source is newer than it."""
+    """Compile and link libgb300gemm.so and its torch binding if any source is
+    newer than they are."""
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding, BUILD)
         objs = list(ex.map(lambda s: _compile(s, BUILD), srcs))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC"] + objs + ["-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     if verbose:
         for s in srcs:
             with open(os.path.join(BUILD, os.path.basename(s) + ".ptxas.txt")) as f:
