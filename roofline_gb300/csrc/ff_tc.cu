@@ -58,10 +58,20 @@ constexpr int kBlockK = 64;
 constexpr int kMaxStages = 12;
 constexpr int kEpiBytes = kEpiWarps * 4096;  // 32 x 16 values, twice, per warp
 constexpr int kStageBudget = 227 * 1024 - 1024 - 256 - kEpiBytes;
-constexpr int kTmemCols = 512;   // two accumulators of at most 256 columns:
-// one plane, one is filled while the other is drained; three planes, the
-// large and the small products
-constexpr int kAccCols = 256;
+constexpr int kTmemCols = 512;
+
+// The accumulators of a tile.  One plane: two, one filled while the other is
+// drained.  Three planes: one or, where they fit, two for the large products
+// (the second is filled while the first is added to the registers), and one
+// for the small ones.
+template <int P, int BN>
+struct Acc {
+  static constexpr int COLS = P == 1 ? 256 : BN;
+  static constexpr int LARGE = P == 1 || 3 * BN <= kTmemCols ? 2 : 1;
+  static constexpr int SMALL = LARGE;  // index of the small products' accumulator
+  static constexpr int COUNT = P == 1 ? 2 : LARGE + 1;
+  static_assert(COUNT * COLS <= kTmemCols, "");
+};
 
 // Waits for the phase of `bar` with the given parity, at most ns; gives up at
 // once when another role of the CTA has.
@@ -365,9 +375,10 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
   const uint32_t stage_bytes = P * (uint32_t)(p.a_bytes + p.b_bytes);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + stages * stage_bytes);
   uint64_t *empty = full + kMaxStages;
-  uint64_t *acc_full = empty + kMaxStages;  // [2]
-  uint64_t *acc_empty = acc_full + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+  using A = Acc<P, BN>;
+  uint64_t *acc_full = empty + kMaxStages;  // [A::COUNT]
+  uint64_t *acc_empty = acc_full + 3;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 3);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   uint8_t *epi = reinterpret_cast<uint8_t *>(full) + 256;
 
@@ -382,7 +393,7 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < A::COUNT; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], CG * kEpiWarps);  // every epilogue warp of the tile
     }
@@ -463,18 +474,21 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
                              ((uint32_t)((CG * 128) >> 4) << 24);
       // 16 along K: 32 bytes of a K-major line, two 8-deep groups MN-major
       const uint64_t astep = p.a_mn ? 2048 >> 4 : 32 >> 4, bstep = p.b_mn ? 2048 >> 4 : 32 >> 4;
-      uint32_t s = 0, ph = 0, used[2] = {0, 0};  // stage; times each accumulator was filled
+      uint32_t s = 0, ph = 0;  // stage and its phase
+      uint32_t filled = 0;     // bit i: the parity of accumulator i's fillings
       // Before accumulator i is filled anew, the epilogue has read it.
       auto take = [&](int i) {
-        ok = ff_wait(&acc_empty[i], (used[i]++ & 1u) ^ 1u, p.wait_ns, abort_flag);
+        ok = ff_wait(&acc_empty[i], ((filled >> i) & 1u) ^ 1u, p.wait_ns, abort_flag);
+        filled ^= 1u << i;
         tc_fence_after();
         return ok;
       };
-      int done = 0;
-      for (int64_t t = worker; ok && t < tiles; t += workers, ++done) {
-        const int acc = P == 1 ? done & 1 : 0;
-        if (P == 1 && !take(acc)) break;
-        const uint32_t d = tmem_base + (uint32_t)(acc * kAccCols);
+      int acc = A::LARGE - 1;  // the accumulator in use, of those taken in turn
+      for (int64_t t = worker; ok && t < tiles; t += workers) {
+        if (P == 1) {
+          acc ^= 1;
+          if (!take(acc)) break;
+        }
         for (int kb = 0; kb < kbs; ++kb) {
           if (!ff_wait(&full[s], ph, p.wait_ns, abort_flag)) {
             ok = false;
@@ -483,21 +497,25 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
           tc_fence_after();
           const uint32_t a = smem_u32(smem) + s * stage_bytes, b = a + P * (uint32_t)p.a_bytes;
           const uint64_t da = tile_desc(a, p.a_mn), db = tile_desc(b, p.b_mn);
-          if (P == 3 && kb % kFlush == 0 && !take(0)) break;
+          if (P == 3 && kb % kFlush == 0) {
+            if (A::LARGE == 2) acc ^= 1;
+            if (!take(acc)) break;
+          }
+          const uint32_t d = tmem_base + (uint32_t)(acc * A::COLS);
           const bool first = P == 1 ? kb == 0 : kb % kFlush == 0;
 #pragma unroll
           for (int kk = 0; kk < kBlockK / 16; ++kk)
             mma_bf16<CG>(d, da + kk * astep, db + kk * bstep, idesc, first && kk == 0 ? 0u : 1u);
           if constexpr (P == 3) {
-            if (kb % kFlush == kFlush - 1 || kb == kbs - 1) commit<CG>(&acc_full[0]);
-            if (kb == 0 && !take(1)) break;
+            if (kb % kFlush == kFlush - 1 || kb == kbs - 1) commit<CG>(&acc_full[acc]);
+            if (kb == 0 && !take(A::SMALL)) break;
 #pragma unroll
             for (int kk = 0; kk < kBlockK / 16; ++kk) {
 #pragma unroll
               for (int sum = P - 1; sum >= 1; --sum) {
 #pragma unroll
                 for (int i = 0; i <= sum; ++i)
-                  mma_bf16<CG>(d + kAccCols, da + kk * astep + (uint64_t)(i * (p.a_bytes >> 4)),
+                  mma_bf16<CG>(tmem_base + (uint32_t)(A::SMALL * A::COLS), da + kk * astep + (uint64_t)(i * (p.a_bytes >> 4)),
                                db + kk * bstep + (uint64_t)((sum - i) * (p.b_bytes >> 4)),
                                idesc, (kb > 0 || kk > 0 || sum < P - 1 || i > 0) ? 1u : 0u);
               }
@@ -506,7 +524,7 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
           commit<CG>(&empty[s]);
           if (++s == stages) s = 0, ph ^= 1;
         }
-        if (ok) commit<CG>(&acc_full[P == 1 ? acc : 1]);
+        if (ok) commit<CG>(&acc_full[P == 1 ? acc : A::SMALL]);
       }
     }
   } else {
@@ -526,10 +544,13 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
     out.ldu = p.ldu;
     out.vec_c = aligned(p.c[0], p.ldc[0], sizeof(T)) && aligned(p.c[1], p.ldc[1], sizeof(T));
     out.vec_gu = aligned(p.g, p.ldg, 4) && aligned(p.u, p.ldu, 4);
-    uint32_t used[2] = {0, 0};
+    uint32_t drained = 0;  // bit i: the parity of accumulator i's drainings
+    int acc = A::LARGE - 1;
     // tcgen05.ld is warp-collective: the warp proceeds or stops as one
     auto wait_full = [&](int i) {
-      ok = __all_sync(0xffffffffu, ff_wait(&acc_full[i], used[i]++ & 1u, p.wait_ns, abort_flag));
+      ok = __all_sync(0xffffffffu,
+                      ff_wait(&acc_full[i], (drained >> i) & 1u, p.wait_ns, abort_flag));
+      drained ^= 1u << i;
       tc_fence_after();
       return ok;
     };
@@ -538,8 +559,7 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
       __syncwarp();
       if (lane == 0) arrive_leader<CG>(&acc_empty[i]);
     };
-    int done = 0;
-    for (int64_t t = worker; ok && t < tiles; t += workers, ++done) {
+    for (int64_t t = worker; ok && t < tiles; t += workers) {
       const TileAt at = tile_at(p, t);
       const int64_t r0 = at.m * (CG * 128) + rank * 128 + quarter * 32;
       const int64_t c0 = at.n * p.out_cols;
@@ -550,9 +570,9 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
       out.g = p.g ? p.g + r0 * p.ldg : nullptr;
       out.u = p.u ? p.u + r0 * p.ldu : nullptr;
       if constexpr (P == 1) {
-        const int acc = done & 1;
+        acc ^= 1;
         if (!wait_full(acc)) break;
-        const uint32_t base = lane_base + (uint32_t)(acc * kAccCols);
+        const uint32_t base = lane_base + (uint32_t)(acc * A::COLS);
         int j = 16 * half;
         if (j >= p.out_cols) release(acc);
 #pragma unroll 1
@@ -574,14 +594,16 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
           for (int k = 0; k < 16; ++k) sum[i][k] = 0.0f;
         const int parts = (kbs + kFlush - 1) / kFlush + 1;
         for (int part = 0; part < parts; ++part) {
-          const int acc = part == parts - 1;
-          if (!wait_full(acc)) break;
+          const bool small = part == parts - 1;
+          if (A::LARGE == 2 && !small) acc ^= 1;
+          const int from = small ? A::SMALL : acc;
+          if (!wait_full(from)) break;
 #pragma unroll
           for (int i = 0; i < BLOCKS; ++i) {
             float x[16];
-            tmem_ld16(lane_base + (uint32_t)(acc * kAccCols + 16 * half + 32 * i), x);
+            tmem_ld16(lane_base + (uint32_t)(from * A::COLS + 16 * half + 32 * i), x);
             tmem_ld_wait();
-            if (i == BLOCKS - 1) release(acc);
+            if (i == BLOCKS - 1) release(from);
 #pragma unroll
             for (int k = 0; k < 16; ++k) sum[i][k] += x[k];
           }
@@ -732,15 +754,16 @@ int launch_cfg(const FfProduct &q, const Choice &ch, const DeviceProps &dp, cuda
 }
 
 // Estimated clocks of one tile.  An MMA (16 along K) takes bn / 2 clocks, or
-// what shared memory needs at 128 bytes a clock for its reads (128 rows of A,
-// the CTA's part of B) and for the copies' writes, which serve the one or six
-// products of their planes.  (GB300: three planes of 128 x 128 ran at 94
-// clocks, 256 x 256 at 128.)  A CTA's loads come at about 55 bytes a clock
-// with the ring full of requests (one token, 128 KB in flight: 28 bytes with
-// half of that).  At the end of a CTA's last tile comes an epilogue that
-// nothing hides.
+// what shared memory needs at 128 bytes a clock for its reads (128 rows of A
+// and all the tile's columns of B, those of the pair's other CTA too) and for
+// the copies' writes, which serve the one or six products of their planes.
+// (GB300, clocks a K block, modelled / measured: one plane 256 x 256 by pairs
+// 640 / 640; three planes 256 x 256 3072 / 3360, 256 x 128 2112 / 2208, 128 x
+// 128 2304 / 2200.)  A CTA's loads come at about 55 bytes a clock with the
+// ring full of requests (one token, 128 KB in flight: 28 bytes with half of
+// that).  At the end of a CTA's last tile comes an epilogue that nothing hides.
 double tile_clocks(const Choice &c, int planes, double kbs) {
-  const double products = planes == 1 ? 1 : 6, rows = 128 + c.bn / c.cg;
+  const double products = planes == 1 ? 1 : 6, rows = 128 + c.bn;
   const double mma = 4 * products * c.bn / 2.0;
   const double smem = 4 * products * rows * 32 / 128 + stage_bytes_of(c, planes) / 128.0;
   const double load = stage_bytes_of(c, planes) / 55.0;

@@ -255,6 +255,23 @@ def test_captured_in_a_graph(ff, dt):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("size", [(256, 256, 128), (1100, 200, 2100)], ids=["one", "pairs"])
+def test_stalled_pipeline_reports_timeout(ff, size, monkeypatch):
+    """With a test hook the producer issues no copy: the waits run out (no copy or MMA is in
+    flight), the status says so, and the next call is right.  Tiles of one CTA and of pairs."""
+    from roofline_gb300 import gemm
+    X, Wg, Wu, _ = _case(3, *size, BF16, "oi")
+    assert gemm.check_status() == gemm.OK
+    with monkeypatch.context() as m:
+        m.setenv("GEMM_DEBUG_STALL_PRODUCER", "1")
+        m.setenv("GEMM_DEBUG_WAIT_LIMIT_NS", "2000000")  # 2 ms
+        ff.gated_ff(X, Wg, Wu)
+        assert gemm.check_status() == gemm.ERR_DEVICE_TIMEOUT
+    assert gemm.check_status() == gemm.OK
+    _check_forward(ff, X, Wg, Wu, "silu")
+    assert gemm.check_status() == gemm.OK
+
+
 # ------------------------------------------------------------------ 4-bit products
 
 def _quant(g, N, K, group, dt, zeros, pad=0):
