@@ -249,8 +249,7 @@ extern "C" int gated_ff_backward(int dtype, int act, int op_w, int64_t M, int64_
     pw.ldc = lddwg;
     pw.ldc2 = lddwu;
   }
-  cudaError_t e = launch_pack(lay.jobs, lay.n, dtype, dp.sm_count, stream);
-  if (e == cudaSuccess) e = launch_dgate(gate, dtype, dp.sm_count, stream);
+  const cudaError_t e = launch_dgate(gate, lay.jobs, lay.n, dtype, dp.sm_count, stream);
   if (e != cudaSuccess) return to_status(e);
   if (dX) st = launch_ff_product(px, dp, stream);
   if (st == GEMM_OK && dWg) st = launch_ff_product(pw, dp, stream);

@@ -70,33 +70,50 @@ struct PackJobs {
   int n;
 };
 
+// Group e of eight values of the jobs.
+template <typename T, int P>
+__device__ __forceinline__ void pack_group(const PackJobs &jobs, int64_t e) {
+  int k = 0;
+  while (e >= jobs.first[k + 1]) ++k;
+  const PackJob &j = jobs.j[k];
+  const int64_t per_row = j.ld_out / 8, at = e - jobs.first[k];
+  const int64_t r = at / per_row, c = (at - r * per_row) * 8;
+  const T *src = static_cast<const T *>(j.src);
+  float v[8];
+  load8(src + r * j.ld, c, j.cols, rows_aligned(src, j.ld), v);
+  store8<P>(v, j.dst + r * j.ld_out + c, j.plane);
+}
+
 template <typename T, int P>
 __global__ void __launch_bounds__(256) ff_pack_kernel(PackJobs jobs) {
   tc::grid_dependency_wait();
   tc::grid_launch_dependents();
   for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < jobs.first[jobs.n];
-       e += gridDim.x * 256ll) {
-    int k = 0;
-    while (e >= jobs.first[k + 1]) ++k;
-    const PackJob &j = jobs.j[k];
-    const int64_t per_row = j.ld_out / 8, at = e - jobs.first[k];
-    const int64_t r = at / per_row, c = (at - r * per_row) * 8;
-    const T *src = static_cast<const T *>(j.src);
-    float v[8];
-    load8(src + r * j.ld, c, j.cols, rows_aligned(src, j.ld), v);
-    store8<P>(v, j.dst + r * j.ld_out + c, j.plane);
-  }
+       e += gridDim.x * 256ll)
+    pack_group<T, P>(jobs, e);
 }
 
+struct GateAndPack {
+  DgateArgs gate;
+  PackJobs jobs;
+};
+
+// The gradients of the gate, and behind them the backward pass's packing,
+// which needs nothing of them: one launch, no tail between the two.
 template <typename T, int P>
-__global__ void __launch_bounds__(256) ff_dgate_kernel(DgateArgs p) {
+__global__ void __launch_bounds__(256) ff_dgate_kernel(GateAndPack q) {
   tc::grid_dependency_wait();
   tc::grid_launch_dependents();
-  const int64_t per_row = p.ld_out / 8, n = p.M * per_row;
+  const DgateArgs &p = q.gate;
+  const int64_t per_row = p.ld_out / 8, n = p.M * per_row, all = n + q.jobs.first[q.jobs.n];
   const T *dh = static_cast<const T *>(p.dh);
   const bool vh = rows_aligned(dh, p.lddh), vg = rows_aligned(p.g, p.ldg),
              vu = rows_aligned(p.u, p.ldu);
-  for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < n; e += gridDim.x * 256ll) {
+  for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < all; e += gridDim.x * 256ll) {
+    if (e >= n) {
+      pack_group<T, P>(q.jobs, e - n);
+      continue;
+    }
     const int64_t r = e / per_row, c = (e - r * per_row) * 8;
     float h[8], g[8], u[8], a[8], d[8];
     load8(dh + r * p.lddh, c, p.F, vh, h);
@@ -137,29 +154,32 @@ int blocks_for(int64_t groups, int sms) {
   return (int)(b < most ? b : most);
 }
 
-}  // namespace
-
-cudaError_t launch_pack(const PackJob *jobs, int n, int dtype, int sms, cudaStream_t s) {
+PackJobs listed(const PackJob *jobs, int n) {
   PackJobs p{};
   for (int k = 0; k < n; ++k) {
-    if (jobs[k].rows <= 0 || jobs[k].ld_out <= 0) continue;
     p.j[p.n] = jobs[k];
     p.first[p.n + 1] = p.first[p.n] + jobs[k].rows * (jobs[k].ld_out / 8);
     ++p.n;
   }
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_pack(const PackJob *jobs, int n, int dtype, int sms, cudaStream_t s) {
+  const PackJobs p = listed(jobs, n);
   if (p.n == 0) return cudaSuccess;
   const int grid = blocks_for(p.first[p.n], sms);
-  if (dtype == GEMM_DT_F32)
-    return launch(ff_pack_kernel<float, 3>, grid, p, s);
+  if (dtype == GEMM_DT_F32) return launch(ff_pack_kernel<float, 3>, grid, p, s);
   return launch(ff_pack_kernel<bf16, 1>, grid, p, s);
 }
 
-cudaError_t launch_dgate(const DgateArgs &p, int dtype, int sms, cudaStream_t s) {
-  if (p.M == 0 || p.F == 0) return cudaSuccess;
-  const int grid = blocks_for(p.M * (p.ld_out / 8), sms);
-  if (dtype == GEMM_DT_F32)
-    return launch(ff_dgate_kernel<float, 3>, grid, p, s);
-  return launch(ff_dgate_kernel<bf16, 1>, grid, p, s);
+cudaError_t launch_dgate(const DgateArgs &p, const PackJob *jobs, int n, int dtype, int sms,
+                         cudaStream_t s) {
+  const GateAndPack q{p, listed(jobs, n)};
+  const int grid = blocks_for(p.M * (p.ld_out / 8) + q.jobs.first[q.jobs.n], sms);
+  if (dtype == GEMM_DT_F32) return launch(ff_dgate_kernel<float, 3>, grid, q, s);
+  return launch(ff_dgate_kernel<bf16, 1>, grid, q, s);
 }
 
 }  // namespace gg

@@ -49,7 +49,8 @@ struct PackJob {
 constexpr int kPackJobs = 3;
 cudaError_t launch_pack(const PackJob *jobs, int n, int dtype, int sms, cudaStream_t s);
 
-// dG = dH * U * act'(G) and dU = dH * act(G), M x F, as such planes.
+// dG = dH * U * act'(G) and dU = dH * act(G), M x F (neither 0), as such
+// planes; and the jobs, in the same launch.
 struct DgateArgs {
   int64_t M, F;
   int act;
@@ -60,6 +61,7 @@ struct DgateArgs {
   bf16 *dg, *du;
   int64_t ld_out, plane;
 };
-cudaError_t launch_dgate(const DgateArgs &p, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_dgate(const DgateArgs &p, const PackJob *jobs, int n, int dtype, int sms,
+                         cudaStream_t s);
 
 }  // namespace gg
