@@ -35,22 +35,60 @@ constexpr int kThreadsFF = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kFlush = 4;
 
+// One product of a launch.
 struct FfParams {
   int64_t M, N;        // output extents (of one matrix)
+  int64_t tiles;
   int kb, segs;        // K blocks of one segment, segments (concat: 2)
-  int tiles_m, tiles_n, batches, group_n;
+  int tiles_m, tiles_n, group_n;
   int a_seg, a_batch, b_seg, b_batch;  // operand = segment * x_seg + batch * x_batch
   int a_mn, b_mn;      // operands stored MN-major
   int bn, out_cols;    // a tile's accumulator and output columns
   int a_bytes, b_bytes;  // one plane of a stage: A's rows and B's columns in this CTA
-  int stages;
   int act;
   void *c[2];
   int64_t ldc[2];
   float *g, *u;
   int64_t ldg, ldu;
+};
+
+// A launch: one product, or the two of a backward pass, whose tiles the
+// workers (CTAs or pairs) take as one list (Walk).
+struct FfLaunch {
+  CUtensorMap map[2][4];  // of a product: A, A', B, B'
+  FfParams p[2];          // the second without tiles if there is one product
+  int stages, stage_bytes;
+  int64_t early_from, early;
   uint64_t wait_ns;
   int stall_producer;  // test hook: the producer issues nothing
+};
+
+// A worker's tiles: those of the first product in turn; then, for the workers
+// from early_from on, which got one fewer of them, as many of the second as
+// that one takes the time of (early); then the rest of the second in turn.
+struct Walk {
+  const FfLaunch &l;
+  int64_t worker, workers, first, done = 0, second;
+  __device__ __forceinline__ Walk(const FfLaunch &launch, int64_t w, int64_t n)
+      : l(launch), worker(w), workers(n), first(w),
+        second((n - launch.early_from) * launch.early + w) {}
+  __device__ __forceinline__ bool next(int &product, int64_t &tile) {
+    if (first < l.p[0].tiles) {
+      product = 0;
+      tile = first;
+      first += workers;
+      return true;
+    }
+    product = 1;
+    if (worker >= l.early_from && done < l.early) {
+      tile = (worker - l.early_from) * l.early + done++;
+      if (tile < l.p[1].tiles) return true;
+      done = l.early;
+    }
+    tile = second;
+    second += workers;
+    return tile < l.p[1].tiles;
+  }
 };
 
 constexpr int kLine = 128;       // bytes of one row of a stage: 64 of K, a swizzle line
@@ -362,17 +400,13 @@ __device__ __forceinline__ TileAt tile_at(const FfParams &p, int64_t t) {
 // is chosen at run time (BN = 0).  P: planes.
 template <int P, int CG, int BN, bool GATED>
 __global__ void __launch_bounds__(kThreadsFF, 1)
-ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CUtensorMap ma1,
-             const __grid_constant__ CUtensorMap mb0, const __grid_constant__ CUtensorMap mb1,
-             const FfParams p) {
+ff_tc_kernel(const __grid_constant__ FfLaunch l) {
   static_assert((P == 1) == (BN == 0), "");
   using T = typename std::conditional<P == 1, bf16, float>::type;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
-  const int bn = P == 1 ? p.bn : BN;
-  const uint32_t stages = (uint32_t)p.stages;
-  const uint32_t stage_bytes = P * (uint32_t)(p.a_bytes + p.b_bytes);
+  const uint32_t stages = (uint32_t)l.stages, stage_bytes = (uint32_t)l.stage_bytes;
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + stages * stage_bytes);
   uint64_t *empty = full + kMaxStages;
   using A = Acc<P, BN>;
@@ -385,8 +419,6 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : cta_rank();
   const int64_t worker = blockIdx.x / CG, workers = gridDim.x / CG;
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.batches;
-  const int kbs = p.kb * p.segs;
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < stages; ++s) {
@@ -400,14 +432,7 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0 && lane == 0) {
-    prefetch_tmap(&ma0);
-    prefetch_tmap(&mb0);
-    if (p.segs > 1 || p.batches > 1 || GATED) {
-      prefetch_tmap(&ma1);
-      prefetch_tmap(&mb1);
-    }
-  }
+  if (warp == 0 && lane < 4) prefetch_tmap(&l.map[0][lane]);
   if (warp == 1) ff_tmem_alloc<CG>(tmem_slot, kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -421,28 +446,36 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
   bool ok = true;
   if (warp == 0) {
     // ---------------- producer: this CTA's rows of A and columns of B
-    if (lane == 0 && !p.stall_producer) {
+    if (lane == 0 && !l.stall_producer) {
       uint32_t s = 0, ph = 1, issued = 0;
       auto take = [&] {
-        ok = ff_wait(&empty[s], ph, p.wait_ns, abort_flag);
+        ok = ff_wait(&empty[s], ph, l.wait_ns, abort_flag);
         return ok;
       };
       auto next = [&] {
         if (++s == stages) s = 0, ph ^= 1;
       };
-      const int b_rows = p.b_bytes / kLine;
-      for (int64_t t = worker; ok && t < tiles; t += workers) {
+      // A product's parameters and maps at addresses that the compiler knows:
+      // issuing a copy through a pointer that it does not took longer than the
+      // tensor core takes for the K block (8192 x 4096 x 11008, MN-major
+      // operands in BF16: 2.1 ms for both products, 1.66 this way).
+      auto load = [&](auto which, int64_t t) {
+        constexpr int product = decltype(which)::value;
+        const FfParams &p = l.p[product];
+        const int kbs = p.kb * p.segs, b_rows = p.b_bytes / kLine;
         const TileAt at = tile_at(p, t);
         const int32_t m0 = (int32_t)(at.m * (CG * 128) + rank * 128);
         const int32_t n0 = (int32_t)(at.n * p.out_cols);
         for (int kb = 0; kb < kbs && take(); ++kb, ++issued, next()) {
-          if (rank == 0) mbar_expect_tx(&full[s], CG * stage_bytes);
+          if (rank == 0) mbar_expect_tx(&full[s], CG * P * (uint32_t)(p.a_bytes + p.b_bytes));
           const uint32_t bar =
               CG == 1 ? smem_u32(&full[s]) : map_to_cta(smem_u32(&full[s]), 0);
           const int seg = kb >= p.kb;
           const int32_t k0 = (kb - seg * p.kb) * kBlockK;
-          const CUtensorMap *ma = seg * p.a_seg + at.batch * p.a_batch ? &ma1 : &ma0;
-          const CUtensorMap *mb = seg * p.b_seg + at.batch * p.b_batch ? &mb1 : &mb0;
+          const CUtensorMap *ma =
+              seg * p.a_seg + at.batch * p.a_batch ? &l.map[product][1] : &l.map[product][0];
+          const CUtensorMap *mb =
+              seg * p.b_seg + at.batch * p.b_batch ? &l.map[product][3] : &l.map[product][2];
           const uint32_t a = smem_u32(smem) + s * stage_bytes, b = a + P * (uint32_t)p.a_bytes;
 #pragma unroll
           for (int q = 0; q < P; ++q) {
@@ -451,13 +484,24 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
             if constexpr (!GATED) {
               load_tile<CG>(bq, mb, bar, p.b_mn, b_rows, n0 + (int)rank * b_rows, k0, q);
             } else if constexpr (CG == 2) {
-              load_tile<CG>(bq, rank ? &mb1 : &mb0, bar, p.b_mn, b_rows, n0, k0, q);
+              load_tile<CG>(bq, rank ? &l.map[product][3] : &l.map[product][2], bar, p.b_mn,
+                            b_rows, n0, k0, q);
             } else {
-              load_tile<CG>(bq, &mb0, bar, p.b_mn, b_rows / 2, n0, k0, q);
-              load_tile<CG>(bq + p.b_bytes / 2, &mb1, bar, p.b_mn, b_rows / 2, n0, k0, q);
+              load_tile<CG>(bq, &l.map[product][2], bar, p.b_mn, b_rows / 2, n0, k0, q);
+              load_tile<CG>(bq + p.b_bytes / 2, &l.map[product][3], bar, p.b_mn, b_rows / 2, n0,
+                            k0, q);
             }
           }
         }
+      };
+      Walk walk(l, worker, workers);
+      int product;
+      int64_t t;
+      while (ok && walk.next(product, t)) {
+        if (GATED || product == 0)
+          load(std::integral_constant<int, 0>(), t);
+        else
+          load(std::integral_constant<int, 1>(), t);
       }
       // Every stage handed back: no load is in flight and no arrival from the
       // pair's MMAs still on its way here.
@@ -469,34 +513,40 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
   } else if (warp == 1) {
     // ---------------- MMA issuer (of the pair)
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.a_mn << 15) |
-                             ((uint32_t)p.b_mn << 16) | ((uint32_t)(bn >> 3) << 17) |
-                             ((uint32_t)((CG * 128) >> 4) << 24);
-      // 16 along K: 32 bytes of a K-major line, two 8-deep groups MN-major
-      const uint64_t astep = p.a_mn ? 2048 >> 4 : 32 >> 4, bstep = p.b_mn ? 2048 >> 4 : 32 >> 4;
       uint32_t s = 0, ph = 0;  // stage and its phase
       uint32_t filled = 0;     // bit i: the parity of accumulator i's fillings
       // Before accumulator i is filled anew, the epilogue has read it.
       auto take = [&](int i) {
-        ok = ff_wait(&acc_empty[i], ((filled >> i) & 1u) ^ 1u, p.wait_ns, abort_flag);
+        ok = ff_wait(&acc_empty[i], ((filled >> i) & 1u) ^ 1u, l.wait_ns, abort_flag);
         filled ^= 1u << i;
         tc_fence_after();
         return ok;
       };
       int acc = A::LARGE - 1;  // the accumulator in use, of those taken in turn
-      for (int64_t t = worker; ok && t < tiles; t += workers) {
+      Walk walk(l, worker, workers);
+      int product;
+      int64_t t;
+      while (ok && walk.next(product, t)) {
+        const FfParams &p = l.p[product];
+        const int bn = P == 1 ? p.bn : BN, a_mn = p.a_mn, b_mn = p.b_mn, kbs = p.kb * p.segs;
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) |
+                               ((uint32_t)b_mn << 16) | ((uint32_t)(bn >> 3) << 17) |
+                               ((uint32_t)((CG * 128) >> 4) << 24);
+        // 16 along K: 32 bytes of a K-major line, two 8-deep groups MN-major
+        const uint64_t astep = a_mn ? 2048 >> 4 : 32 >> 4, bstep = b_mn ? 2048 >> 4 : 32 >> 4;
+        const uint32_t a_plane = (uint32_t)p.a_bytes, b_plane = (uint32_t)p.b_bytes;
         if (P == 1) {
           acc ^= 1;
           if (!take(acc)) break;
         }
         for (int kb = 0; kb < kbs; ++kb) {
-          if (!ff_wait(&full[s], ph, p.wait_ns, abort_flag)) {
+          if (!ff_wait(&full[s], ph, l.wait_ns, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(smem) + s * stage_bytes, b = a + P * (uint32_t)p.a_bytes;
-          const uint64_t da = tile_desc(a, p.a_mn), db = tile_desc(b, p.b_mn);
+          const uint32_t a = smem_u32(smem) + s * stage_bytes, b = a + P * a_plane;
+          const uint64_t da = tile_desc(a, a_mn), db = tile_desc(b, b_mn);
           if (P == 3 && kb % kFlush == 0) {
             if (A::LARGE == 2) acc ^= 1;
             if (!take(acc)) break;
@@ -515,9 +565,10 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
               for (int sum = P - 1; sum >= 1; --sum) {
 #pragma unroll
                 for (int i = 0; i <= sum; ++i)
-                  mma_bf16<CG>(tmem_base + (uint32_t)(A::SMALL * A::COLS), da + kk * astep + (uint64_t)(i * (p.a_bytes >> 4)),
-                               db + kk * bstep + (uint64_t)((sum - i) * (p.b_bytes >> 4)),
-                               idesc, (kb > 0 || kk > 0 || sum < P - 1 || i > 0) ? 1u : 0u);
+                  mma_bf16<CG>(tmem_base + (uint32_t)(A::SMALL * A::COLS),
+                               da + kk * astep + (uint64_t)(i * (a_plane >> 4)),
+                               db + kk * bstep + (uint64_t)((sum - i) * (b_plane >> 4)), idesc,
+                               (kb > 0 || kk > 0 || sum < P - 1 || i > 0) ? 1u : 0u);
               }
             }
           }
@@ -538,18 +589,12 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
     };
     Writer<T, GATED> out;
     out.st = st;
-    out.N = p.N;
-    out.act = p.act;
-    out.ldg = p.ldg;
-    out.ldu = p.ldu;
-    out.vec_c = aligned(p.c[0], p.ldc[0], sizeof(T)) && aligned(p.c[1], p.ldc[1], sizeof(T));
-    out.vec_gu = aligned(p.g, p.ldg, 4) && aligned(p.u, p.ldu, 4);
     uint32_t drained = 0;  // bit i: the parity of accumulator i's drainings
     int acc = A::LARGE - 1;
     // tcgen05.ld is warp-collective: the warp proceeds or stops as one
     auto wait_full = [&](int i) {
       ok = __all_sync(0xffffffffu,
-                      ff_wait(&acc_full[i], (drained >> i) & 1u, p.wait_ns, abort_flag));
+                      ff_wait(&acc_full[i], (drained >> i) & 1u, l.wait_ns, abort_flag));
       drained ^= 1u << i;
       tc_fence_after();
       return ok;
@@ -559,13 +604,24 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
       __syncwarp();
       if (lane == 0) arrive_leader<CG>(&acc_empty[i]);
     };
-    for (int64_t t = worker; ok && t < tiles; t += workers) {
+    Walk walk(l, worker, workers);
+    int product;
+    int64_t t;
+    while (ok && walk.next(product, t)) {
+      const FfParams &p = l.p[product];
+      const int out_cols = p.out_cols;
+      out.N = p.N;
+      out.act = p.act;
+      out.ldg = p.ldg;
+      out.ldu = p.ldu;
       const TileAt at = tile_at(p, t);
       const int64_t r0 = at.m * (CG * 128) + rank * 128 + quarter * 32;
-      const int64_t c0 = at.n * p.out_cols;
+      const int64_t c0 = at.n * out_cols;
       out.rows = (int)(p.M - r0 < 32 ? p.M - r0 : 32);
       out.ldc = p.ldc[at.batch];
       out.c = static_cast<T *>(p.c[at.batch]);
+      out.vec_c = aligned(out.c, out.ldc, sizeof(T));
+      out.vec_gu = aligned(p.g, p.ldg, 4) && aligned(p.u, p.ldu, 4);
       if (out.c) out.c += r0 * out.ldc;
       out.g = p.g ? p.g + r0 * p.ldg : nullptr;
       out.u = p.u ? p.u + r0 * p.ldu : nullptr;
@@ -574,14 +630,14 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
         if (!wait_full(acc)) break;
         const uint32_t base = lane_base + (uint32_t)(acc * A::COLS);
         int j = 16 * half;
-        if (j >= p.out_cols) release(acc);
+        if (j >= out_cols) release(acc);
 #pragma unroll 1
-        for (; j < p.out_cols; j += 32) {
+        for (; j < out_cols; j += 32) {
           float v[16], w[16];
           tmem_ld16(base + (uint32_t)j, v);
-          if constexpr (GATED) tmem_ld16(base + (uint32_t)(p.out_cols + j), w);
+          if constexpr (GATED) tmem_ld16(base + (uint32_t)(out_cols + j), w);
           tmem_ld_wait();
-          if (j + 32 >= p.out_cols) release(acc);
+          if (j + 32 >= out_cols) release(acc);
           out.block(c0 + j, v, w);
         }
       } else {
@@ -592,7 +648,7 @@ ff_tc_kernel(const __grid_constant__ CUtensorMap ma0, const __grid_constant__ CU
         for (int i = 0; i < BLOCKS; ++i)
 #pragma unroll
           for (int k = 0; k < 16; ++k) sum[i][k] = 0.0f;
-        const int parts = (kbs + kFlush - 1) / kFlush + 1;
+        const int parts = (p.kb * p.segs + kFlush - 1) / kFlush + 1;
         for (int part = 0; part < parts; ++part) {
           const bool small = part == parts - 1;
           if (A::LARGE == 2 && !small) acc ^= 1;
@@ -679,14 +735,12 @@ int stage_bytes_of(const Choice &c, int planes) {
   return planes * (c.a_rows + c.bn / c.cg) * kLine;
 }
 
-template <int P, int CG, int BN, bool GATED>
-int launch_cfg(const FfProduct &q, const Choice &ch, const DeviceProps &dp, cudaStream_t s) {
+FfParams params_of(const FfProduct &q, const Choice &ch) {
   FfParams p{};
   p.M = q.M;
   p.N = q.N;
   p.kb = (int)ceil_div(q.K, kBlockK);
   p.segs = q.kind == kFfConcat ? 2 : 1;
-  p.batches = q.kind == kFfBatch ? 2 : 1;
   p.a_seg = p.b_seg = q.kind == kFfConcat;
   p.a_batch = q.kind == kFfBatch && q.a_two;
   p.b_batch = q.kind == kFfBatch && q.b_two;
@@ -701,32 +755,143 @@ int launch_cfg(const FfProduct &q, const Choice &ch, const DeviceProps &dp, cuda
   p.u = q.u;
   p.ldg = q.ldg;
   p.ldu = q.ldu;
-  p.wait_ns = env_u64("GEMM_DEBUG_WAIT_LIMIT_NS", 2000000000ull);
-  p.stall_producer = (int)env_u64("GEMM_DEBUG_STALL_PRODUCER", 0);
-  p.tiles_m = (int)ceil_div(q.M, CG * 128);
   p.bn = ch.bn;
-  p.out_cols = GATED ? ch.bn / 2 : ch.bn;
+  p.out_cols = q.kind == kFfGated ? ch.bn / 2 : ch.bn;
   p.a_bytes = ch.a_rows * kLine;
-  p.b_bytes = ch.bn / CG * kLine;
-  const int stage = stage_bytes_of(ch, P);
-  p.stages = kStageBudget / stage < kMaxStages ? kStageBudget / stage : kMaxStages;
-  const int smem = p.stages * stage + 1024 + 256 + kEpiBytes;
+  p.b_bytes = ch.bn / ch.cg * kLine;
+  p.tiles_m = (int)ceil_div(q.M, ch.cg * 128);
   p.tiles_n = (int)ceil_div(q.N, p.out_cols);
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.batches;
-  int64_t workers = dp.sm_count / CG;
-  if (workers > tiles) workers = tiles;
   p.group_n = p.tiles_n < 8 ? p.tiles_n : 8;
+  p.tiles = (int64_t)p.tiles_m * p.tiles_n * (q.kind == kFfBatch ? 2 : 1);
+  return p;
+}
 
-  // columns of B one load brings: the gated form takes each half of a single
-  // CTA's columns, or all of one CTA of a pair, from one of the two matrices
-  const int b_load = GATED && CG == 1 ? ch.bn / 2 : ch.bn / CG;
-  CUtensorMap ma[2], mb[2];
-  for (int i = 0; i < 2; ++i) {
-    const FfOperand &a = q.a[i].p ? q.a[i] : q.a[0], &b = q.b[i].p ? q.b[i] : q.b[0];
-    if (!encode(&ma[i], a, P, a.mn_major ? 64 : ch.a_rows) ||
-        !encode(&mb[i], b, P, b.mn_major ? 64 : b_load))
-      return GEMM_ERR_UNSUPPORTED;
+// Estimated clocks of one tile.  An MMA (16 along K) takes bn / 2 clocks, or
+// what shared memory needs at 128 bytes a clock for its reads (128 rows of A
+// and all the tile's columns of B, those of the pair's other CTA too) and for
+// the copies' writes, which serve the one or six products of their planes.
+// (GB300, clocks a K block, modelled / measured: one plane 256 x 256 by pairs
+// 640 / 640; three planes 256 x 256 3072 / 3360, 256 x 128 2112 / 2208, 128 x
+// 128 2304 / 2200.)  A CTA's loads come at about 55 bytes a clock with the
+// ring full of requests (one token, 128 KB in flight: 28 bytes with half of
+// that).
+double tile_clocks(const FfProduct &q, const Choice &c) {
+  const double kbs = (double)ceil_div(q.K, kBlockK) * (q.kind == kFfConcat ? 2 : 1);
+  const double products = q.planes == 1 ? 1 : 6, rows = 128 + c.bn;
+  const double mma = 4 * products * c.bn / 2.0;
+  const double smem = 4 * products * rows * 32 / 128 + stage_bytes_of(c, q.planes) / 128.0;
+  const double load = stage_bytes_of(c, q.planes) / 55.0;
+  const double most = mma > smem ? mma : smem;
+  return kbs * (most > load ? most : load);
+}
+
+int64_t tiles_of(const FfProduct &q, const Choice &c) {
+  return ceil_div(q.M, c.cg * 128) * ceil_div(q.N, q.kind == kFfGated ? c.bn / 2 : c.bn) *
+         (q.kind == kFfBatch ? 2 : 1);
+}
+
+// Whether the product's operands can be cut into such tiles.  Three planes
+// come in a few sizes, one plane in every width that the operands' storage
+// lets TMA cut: blocks of 16 output columns, MN-major ones of 64, from one
+// matrix or one half.
+bool tile_fits(const FfProduct &q, int cg, int bn) {
+  const bool gated = q.kind == kFfGated;
+  const int parts = gated || cg == 2 ? 2 : 1;  // loads that share the columns
+  const int unit = q.b[0].mn_major ? 64 * parts : gated || cg == 2 ? 32 : 16;
+  if (bn % unit != 0) return false;
+  if (q.planes == 1) return true;
+  return cg == 2 ? bn == 256 || bn == 128 : bn == 128 || (bn == 64 && !gated);
+}
+
+Choice choice_of(const FfProduct &q, int cg, int bn) {
+  const bool few = cg == 1 && !q.a[0].mn_major && q.M < 128;
+  return {cg, bn, few ? (int)ceil_div(q.M, 8) * 8 : 128};
+}
+
+// The tiles of n products (one, or two of one launch) with the least
+// estimated time: whole waves of one product's tiles, or all tiles spread
+// evenly and one more of the second product; and for a CTA's last tile an
+// epilogue that nothing hides, about 30 clocks a column.  Two products share
+// the CTAs of a tile, and with three planes the kernel's columns.
+void choose(const FfProduct *q, int n, int sms, Choice *best) {
+  double least = 0.0;
+  for (int cg = 2; cg >= 1; --cg) {
+    const double workers = sms / cg;
+    if (n == 1 || q[0].planes == 3) {
+      for (int bn = 256; bn >= 32; bn -= 16) {
+        if (!tile_fits(q[0], cg, bn) || (n == 2 && !tile_fits(q[1], cg, bn))) continue;
+        Choice c[2];
+        double t = 30.0 * bn, all = 0.0, clocks = 0.0;
+        for (int i = 0; i < n; ++i) {
+          c[i] = choice_of(q[i], cg, bn);
+          clocks = tile_clocks(q[i], c[i]);
+          const double tiles = (double)tiles_of(q[i], c[i]);
+          all += clocks * (n == 1 ? (double)ceil_div((int64_t)tiles, (int64_t)workers) : tiles / workers);
+        }
+        t += all + (n == 2 ? clocks : 0.0);
+        if (least == 0.0 || t < least) {
+          least = t;
+          for (int i = 0; i < n; ++i) best[i] = c[i];
+        }
+      }
+    } else {
+      // each product's width by itself: what it adds to every worker's time
+      Choice c[2];
+      double t = 0.0;
+      for (int i = 0; i < 2; ++i) {
+        double part = 0.0;
+        for (int bn = 256; bn >= 32; bn -= 16) {
+          if (!tile_fits(q[i], cg, bn)) continue;
+          const Choice x = choice_of(q[i], cg, bn);
+          const double clocks = tile_clocks(q[i], x);
+          const double v = clocks * (double)tiles_of(q[i], x) / workers + (i == 1 ? clocks : 0.0) +
+                           15.0 * bn;
+          if (part == 0.0 || v < part) {
+            part = v;
+            c[i] = x;
+          }
+        }
+        t += part;
+      }
+      if (least == 0.0 || t < least) {
+        least = t;
+        best[0] = c[0];
+        best[1] = c[1];
+      }
+    }
   }
+}
+
+template <int P, int CG, int BN, bool GATED>
+int launch_cfg(const FfProduct *q, int n, const Choice *ch, const DeviceProps &dp,
+               cudaStream_t s) {
+  FfLaunch l{};
+  int64_t workers = dp.sm_count / CG, tiles = 0;
+  double clocks[2] = {0.0, 0.0};
+  for (int i = 0; i < n; ++i) {
+    l.p[i] = params_of(q[i], ch[i]);
+    tiles += l.p[i].tiles;
+    clocks[i] = tile_clocks(q[i], ch[i]);
+    const int stage = stage_bytes_of(ch[i], P);
+    if (stage > l.stage_bytes) l.stage_bytes = stage;
+    // columns of B one load brings: the gated form takes each half of a single
+    // CTA's columns, or all of one CTA of a pair, from one of the two matrices
+    const int b_load = GATED && CG == 1 ? ch[i].bn / 2 : ch[i].bn / CG;
+    for (int k = 0; k < 2; ++k) {
+      const FfOperand &a = q[i].a[k].p ? q[i].a[k] : q[i].a[0];
+      const FfOperand &b = q[i].b[k].p ? q[i].b[k] : q[i].b[0];
+      if (!encode(&l.map[i][k], a, P, a.mn_major ? 64 : ch[i].a_rows) ||
+          !encode(&l.map[i][2 + k], b, P, b.mn_major ? 64 : b_load))
+        return GEMM_ERR_UNSUPPORTED;
+    }
+  }
+  if (workers > tiles) workers = tiles;
+  l.stages = kStageBudget / l.stage_bytes < kMaxStages ? kStageBudget / l.stage_bytes : kMaxStages;
+  l.early_from = l.p[0].tiles % workers;
+  l.early = n == 2 && l.early_from > 0 ? (int64_t)(clocks[0] / clocks[1]) : 0;
+  l.wait_ns = env_u64("GEMM_DEBUG_WAIT_LIMIT_NS", 2000000000ull);
+  l.stall_producer = (int)env_u64("GEMM_DEBUG_STALL_PRODUCER", 0);
+
   auto kern = ff_tc_kernel<P, CG, BN, GATED>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
       cudaSuccess) {
@@ -742,88 +907,44 @@ int launch_cfg(const FfProduct &q, const Choice &ch, const DeviceProps &dp, cuda
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(workers * CG));
   lc.blockDim = dim3(kThreadsFF);
-  lc.dynamicSmemBytes = smem;
+  lc.dynamicSmemBytes = l.stages * l.stage_bytes + 1024 + 256 + kEpiBytes;
   lc.stream = s;
   lc.attrs = attr;
   lc.numAttrs = 2;
-  if (cudaLaunchKernelEx(&lc, kern, ma[0], ma[1], mb[0], mb[1], p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&lc, kern, l) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
   return GEMM_OK;
 }
 
-// Estimated clocks of one tile.  An MMA (16 along K) takes bn / 2 clocks, or
-// what shared memory needs at 128 bytes a clock for its reads (128 rows of A
-// and all the tile's columns of B, those of the pair's other CTA too) and for
-// the copies' writes, which serve the one or six products of their planes.
-// (GB300, clocks a K block, modelled / measured: one plane 256 x 256 by pairs
-// 640 / 640; three planes 256 x 256 3072 / 3360, 256 x 128 2112 / 2208, 128 x
-// 128 2304 / 2200.)  A CTA's loads come at about 55 bytes a clock with the
-// ring full of requests (one token, 128 KB in flight: 28 bytes with half of
-// that).  At the end of a CTA's last tile comes an epilogue that nothing hides.
-double tile_clocks(const Choice &c, int planes, double kbs) {
-  const double products = planes == 1 ? 1 : 6, rows = 128 + c.bn;
-  const double mma = 4 * products * c.bn / 2.0;
-  const double smem = 4 * products * rows * 32 / 128 + stage_bytes_of(c, planes) / 128.0;
-  const double load = stage_bytes_of(c, planes) / 55.0;
-  const double most = mma > smem ? mma : smem;
-  return kbs * (most > load ? most : load);
-}
-
-// The tile with the least estimated time.  Three planes come in a few sizes,
-// one plane in every width that its operands' storage lets TMA cut: blocks of
-// 16 output columns, MN-major ones of 64, from one matrix or one half.
-Choice choose(const FfProduct &q, int sms) {
-  const bool gated = q.kind == kFfGated;
-  const double kbs = (double)ceil_div(q.K, kBlockK) * (q.kind == kFfConcat ? 2 : 1);
-  Choice best{};
-  double least = 0.0;
-  for (int cg = 2; cg >= 1; --cg) {
-    const int parts = gated || cg == 2 ? 2 : 1;  // loads that share the columns
-    const int unit = q.b[0].mn_major ? 64 * parts : gated || cg == 2 ? 32 : 16;
-    for (int bn = 256; bn >= 32; bn -= 16) {
-      if (bn % unit != 0) continue;
-      if (q.planes == 3 && bn != 256 && bn != 128 && bn != 64) continue;
-      if (q.planes == 3 && (cg == 2 ? bn == 64 : bn == 256 || (gated && bn == 64))) continue;
-      const int a_rows = cg == 1 && !q.a[0].mn_major && q.M < 128 ? (int)ceil_div(q.M, 8) * 8 : 128;
-      const Choice c{cg, bn, a_rows};
-      const int64_t tiles = ceil_div(q.M, cg * 128) * ceil_div(q.N, gated ? bn / 2 : bn) *
-                            (q.kind == kFfBatch ? 2 : 1);
-      const double t = (double)ceil_div(tiles, sms / cg) * tile_clocks(c, q.planes, kbs) + 30.0 * bn;
-      if (least == 0.0 || t < least) {
-        least = t;
-        best = c;
-      }
-    }
-  }
-  return best;
-}
-
 template <int P, bool GATED>
-int launch_any(const FfProduct &q, const DeviceProps &dp, cudaStream_t s) {
-  const Choice c = choose(q, dp.sm_count);
+int launch_any(const FfProduct *q, int n, const DeviceProps &dp, cudaStream_t s) {
+  Choice c[2];
+  choose(q, n, dp.sm_count, c);
   if constexpr (P == 1) {
-    return c.cg == 2 ? launch_cfg<1, 2, 0, GATED>(q, c, dp, s)
-                     : launch_cfg<1, 1, 0, GATED>(q, c, dp, s);
+    return c[0].cg == 2 ? launch_cfg<1, 2, 0, GATED>(q, n, c, dp, s)
+                        : launch_cfg<1, 1, 0, GATED>(q, n, c, dp, s);
   } else {
-    if (c.cg == 2)
-      return c.bn == 256 ? launch_cfg<3, 2, 256, GATED>(q, c, dp, s)
-                         : launch_cfg<3, 2, 128, GATED>(q, c, dp, s);
+    if (c[0].cg == 2)
+      return c[0].bn == 256 ? launch_cfg<3, 2, 256, GATED>(q, n, c, dp, s)
+                            : launch_cfg<3, 2, 128, GATED>(q, n, c, dp, s);
     if constexpr (!GATED)
-      if (c.bn == 64) return launch_cfg<3, 1, 64, false>(q, c, dp, s);
-    return launch_cfg<3, 1, 128, GATED>(q, c, dp, s);
+      if (c[0].bn == 64) return launch_cfg<3, 1, 64, false>(q, n, c, dp, s);
+    return launch_cfg<3, 1, 128, GATED>(q, n, c, dp, s);
   }
 }
 
 }  // namespace
 
-int launch_ff_product(const FfProduct &q, const DeviceProps &dp, cudaStream_t s) {
+int launch_ff_products(const FfProduct *q, int n, const DeviceProps &dp, cudaStream_t s) {
   if (!tc_supported(dp)) return GEMM_ERR_UNSUPPORTED;
   if (!get_encoder()) return GEMM_ERR_CUDA;
-  if (q.planes == 1)
-    return q.kind == kFfGated ? launch_any<1, true>(q, dp, s) : launch_any<1, false>(q, dp, s);
-  return q.kind == kFfGated ? launch_any<3, true>(q, dp, s) : launch_any<3, false>(q, dp, s);
+  if (q[0].planes == 1)
+    return q[0].kind == kFfGated ? launch_any<1, true>(q, n, dp, s)
+                                 : launch_any<1, false>(q, n, dp, s);
+  return q[0].kind == kFfGated ? launch_any<3, true>(q, n, dp, s)
+                               : launch_any<3, false>(q, n, dp, s);
 }
 
 // Called on a synchronised stream.

@@ -34,8 +34,9 @@ struct FfProduct {
   float *g, *u;
   int64_t ldg, ldu;
 };
-// Enqueues it; returns a GEMM_* status.
-int launch_ff_product(const FfProduct &p, const DeviceProps &dp, cudaStream_t s);
+// Enqueues n products in one launch: one, or two that are not gated and of as
+// many planes, the one with longer sums first.  Returns a GEMM_* status.
+int launch_ff_products(const FfProduct *p, int n, const DeviceProps &dp, cudaStream_t s);
 int ff_read_and_clear_status();
 
 // Lays one matrix (rows x cols, row stride ld, FP32 or BF16) out as BF16
