@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -79,6 +80,23 @@ __device__ __forceinline__ void with_act(int act, F f) {
 inline bool dtype_known(int d) { return d == GEMM_DT_F32 || d == GEMM_DT_BF16; }
 inline bool act_known(int a) { return a >= GEMM_ACT_SILU && a <= GEMM_ACT_RELU; }
 inline size_t dtype_size(int d) { return d == GEMM_DT_F32 ? 4 : 2; }
+
+// Lets a kernel use `bytes` of dynamic shared memory on device `dev`.  The
+// attribute stays with the kernel, so each launcher keeps one Once for its
+// kernel and sets it once for each device: half a microsecond of every later
+// call.  (Two threads that set it at once do no harm.)
+struct Once {
+  std::atomic<bool> done[64] = {};
+};
+template <typename K>
+cudaError_t allow_shared_memory(Once &once, K kern, int bytes, int dev) {
+  const bool known = dev >= 0 && dev < 64;
+  if (known && once.done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) once.done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
 
 // abi.cu
 int current_device(int *dev);

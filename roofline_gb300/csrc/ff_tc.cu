@@ -893,8 +893,8 @@ int launch_cfg(const FfProduct *q, int n, const Choice *ch, const DeviceProps &d
   l.stall_producer = (int)env_u64("GEMM_DEBUG_STALL_PRODUCER", 0);
 
   auto kern = ff_tc_kernel<P, CG, BN, GATED>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-      cudaSuccess) {
+  static Once once;
+  if (allow_shared_memory(once, kern, 227 * 1024, dp.device) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }

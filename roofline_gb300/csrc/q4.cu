@@ -449,16 +449,16 @@ q4_kernel(const Q4Args p) {
 }
 
 template <typename T, int W, int TI, int NT, bool GATED>
-cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, int sms) {
+cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, const DeviceProps &dp) {
   using Cfg = Q4Cfg<T, W, TI, NT, GATED>;
   static_assert(Cfg::WARP_BYTES * Cfg::MAX_WARPS <= 227 * 1024 && Cfg::MAX_WARPS >= 4, "");
   auto kern = q4_kernel<T, W, TI, NT, GATED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg::WARP_BYTES * Cfg::MAX_WARPS);
+  static Once once;
+  const cudaError_t e = allow_shared_memory(once, kern, Cfg::WARP_BYTES * Cfg::MAX_WARPS, dp.device);
   if (e != cudaSuccess) return e;
   // Warps: as many as fill the SMs, but no more than there are steps.
   const int64_t ctas = ceil_div(p.N, Cfg::ROWS), steps = ceil_div(p.K, Cfg::STEP);
-  int64_t warps = (int64_t)Cfg::SM_WARPS * sms / ctas;
+  int64_t warps = (int64_t)Cfg::SM_WARPS * dp.sm_count / ctas;
   warps = warps < 4 ? 4 : warps > Cfg::MAX_WARPS ? Cfg::MAX_WARPS : warps;
   if (warps > steps) warps = steps < 1 ? 1 : steps;
   kern<<<dim3((unsigned)ctas, (unsigned)ceil_div(p.M, kTileTokens<T> * NT)), (unsigned)warps * 32,
@@ -469,7 +469,7 @@ cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, int sms) {
 // Two tiles for one tile of columns; four for two, whose x is then loaded
 // half as often.
 template <typename T, int W, bool GATED>
-cudaError_t pick_tiles(Q4Args p, cudaStream_t s, int sms) {
+cudaError_t pick_tiles(Q4Args p, cudaStream_t s, const DeviceProps &dp) {
   constexpr int parts = 8 / W, bytes = parts * (int)sizeof(T) < 16 ? parts * (int)sizeof(T) : 16;
   uintptr_t q = 0, sc = (uintptr_t)p.groups * sizeof(T);
   for (int k = 0; k < (GATED ? 2 : 1); ++k) {
@@ -478,15 +478,15 @@ cudaError_t pick_tiles(Q4Args p, cudaStream_t s, int sms) {
   }
   p.aligned = q % 16 == 0;
   p.scales_aligned = p.group == 32 * W && sc % bytes == 0 && bytes >= 4;
-  return p.M > kTileTokens<T> ? launch_q4<T, W, 4, 2, GATED>(p, s, sms)
-                              : launch_q4<T, W, 2, 1, GATED>(p, s, sms);
+  return p.M > kTileTokens<T> ? launch_q4<T, W, 4, 2, GATED>(p, s, dp)
+                              : launch_q4<T, W, 2, 1, GATED>(p, s, dp);
 }
 
 template <typename T, bool GATED>
-cudaError_t pick_group(const Q4Args &p, cudaStream_t s, int sms) {
-  return p.group == 32   ? pick_tiles<T, 1, GATED>(p, s, sms)
-         : p.group == 64 ? pick_tiles<T, 2, GATED>(p, s, sms)
-                         : pick_tiles<T, 4, GATED>(p, s, sms);
+cudaError_t pick_group(const Q4Args &p, cudaStream_t s, const DeviceProps &dp) {
+  return p.group == 32   ? pick_tiles<T, 1, GATED>(p, s, dp)
+         : p.group == 64 ? pick_tiles<T, 2, GATED>(p, s, dp)
+                         : pick_tiles<T, 4, GATED>(p, s, dp);
 }
 
 bool side_ok(const Q4Side &w, const Q4Args &p, int dtype) {
@@ -517,17 +517,17 @@ int run_q4(int dtype, int sides, Q4Args p, cudaStream_t stream) {
   int dev = -1;
   const int st = current_device(&dev);
   if (st != GEMM_OK) return st;
-  const int sms = props_of(dev).sm_count;
+  const DeviceProps &dp = props_of(dev);
   p.mask = 0x000f000f;
   p.group_shift = p.group == 32 ? 5 : p.group == 64 ? 6 : p.group == 128 ? 7 : 8;
   p.vec_x = ((reinterpret_cast<uintptr_t>(p.x) | (p.M > 1 ? (uintptr_t)p.ldx * size : 0)) & 15) == 0;
   cudaError_t e;
   if (dtype == GEMM_DT_F32)
-    e = sides == 2 ? pick_group<float, true>(p, stream, sms)
-                   : pick_group<float, false>(p, stream, sms);
+    e = sides == 2 ? pick_group<float, true>(p, stream, dp)
+                   : pick_group<float, false>(p, stream, dp);
   else
-    e = sides == 2 ? pick_group<bf16, true>(p, stream, sms)
-                   : pick_group<bf16, false>(p, stream, sms);
+    e = sides == 2 ? pick_group<bf16, true>(p, stream, dp)
+                   : pick_group<bf16, false>(p, stream, dp);
   return to_status(e);
 }
 
