@@ -1,5 +1,6 @@
 // The gated feed-forward block and its gradients: argument checks, workspace
 // and the launches (include/gb300_gemm.h, gated_ff and gated_ff_backward).
+#include "ff_few.cuh"
 #include "ff_tc.cuh"
 
 namespace gg {
@@ -80,6 +81,22 @@ cudaError_t zero(void *p, int64_t ld, int64_t rows, int64_t cols, size_t size, c
   return cudaMemset2DAsync(p, ld * size, 0, cols * size, rows, s);
 }
 
+// FP32 calls that the CUDA cores take (ff_few.cu).  GB300, 4096 x 11008, us by
+// the tensor cores / the CUDA cores, for 1, 8 and 16 tokens; weights D x F:
+// block 297/94, 297/270, 298/504, gradients 808/167, 807/277, 814/451; weights
+// F x D: block 302/86, 301/137, 300/228, gradients 801/168, 801/427, 808/745.
+bool few_tokens(int dtype, int64_t M, bool backward, int op_w) {
+  return dtype == GEMM_DT_F32 && M <= (backward || op_w == GEMM_OP_T ? kFewTokens : kFewTokens / 2);
+}
+
+// dG and dU as floats, then the sums of dX's parts.
+uint64_t few_gate_bytes(int64_t M, int64_t F) {
+  return align256((uint64_t)M * (uint64_t)round8(F) * 4);
+}
+uint64_t few_backward_bytes(int op_w, int64_t M, int64_t D, int64_t F, int sms) {
+  return 2 * few_gate_bytes(M, F) + few_bytes(M, D, F, op_w == GEMM_OP_N, sms);
+}
+
 // The caller's workspace, or the library's.
 int take_workspace(int dev, uint64_t need, void *workspace, size_t ws_bytes, void **out) {
   *out = nullptr;
@@ -102,6 +119,11 @@ int gated_ff_workspace(int backward, int dtype, int op_w, int64_t M, int64_t D, 
   if (!bytes) return GEMM_ERR_INVALID_ARG;
   const int st = check_sizes(dtype, GEMM_ACT_SILU, op_w, M, D, F);
   if (st != GEMM_OK) return st;
+  if (few_tokens(dtype, M, backward != 0, op_w)) {
+    *bytes = backward ? few_backward_bytes(op_w, M, D, F, current_props().sm_count)
+                      : few_bytes(M, F, D, op_w == GEMM_OP_T, current_props().sm_count);
+    return GEMM_OK;
+  }
   const bool packed = dtype == GEMM_DT_F32 || !aligned;
   *bytes = packed ? plane_bytes(dtype, M, D) + 2 * plane_bytes(dtype, op_w == GEMM_OP_N ? D : F,
                                                                op_w == GEMM_OP_N ? F : D)
@@ -140,6 +162,31 @@ int gated_ff(int dtype, int act, int op_w, int64_t M, int64_t D, int64_t F, cons
   }
   const Stored x{X, M, D, ldx}, wg = weight(Wg, ldwg, op_w, D, F), wu = weight(Wu, ldwu, op_w, D, F);
   void *ws = nullptr;
+  if (few_tokens(dtype, M, false, op_w)) {
+    st = take_workspace(dev, few_bytes(M, F, D, op_w == GEMM_OP_T, dp.sm_count), workspace, ws_bytes,
+                        &ws);
+    if (st != GEMM_OK) return st;
+    FewArgs p{};
+    p.M = M;
+    p.N = F;
+    p.K = D;
+    p.gated = 1;
+    p.act = act;
+    p.rows_are_outputs = op_w == GEMM_OP_T;
+    p.a[0] = p.a[1] = static_cast<const float *>(X);
+    p.lda = ldx;
+    p.b[0] = static_cast<const float *>(Wg);
+    p.b[1] = static_cast<const float *>(Wu);
+    p.ldb[0] = ldwg;
+    p.ldb[1] = ldwu;
+    p.c = static_cast<float *>(H);
+    p.ldc = ldh;
+    p.g = G;
+    p.u = U;
+    p.ldg = ldg;
+    p.ldu = ldu;
+    return to_status(launch_few(p, ws, dp.sm_count, stream));
+  }
   st = take_workspace(dev, pack_bytes(dtype, x) + pack_bytes(dtype, wg) + pack_bytes(dtype, wu),
                       workspace, ws_bytes, &ws);
   if (st != GEMM_OK) return st;
@@ -202,6 +249,52 @@ extern "C" int gated_ff_backward(int dtype, int act, int op_w, int64_t M, int64_
     return to_status(e);
   }
   const Stored x{X, M, D, ldx}, wg = weight(Wg, ldwg, op_w, D, F), wu = weight(Wu, ldwu, op_w, D, F);
+  if (few_tokens(dtype, M, true, op_w)) {
+    void *few = nullptr;
+    st = take_workspace(dev, few_backward_bytes(op_w, M, D, F, dp.sm_count), workspace, ws_bytes, &few);
+    if (st != GEMM_OK) return st;
+    const uint64_t part = few_gate_bytes(M, F);
+    uint8_t *at = static_cast<uint8_t *>(few);
+    const float *dg = reinterpret_cast<float *>(at), *du = reinterpret_cast<float *>(at + part);
+    const DgateArgs gate{M, F, act, dH, lddh, G, U, ldg, ldu, reinterpret_cast<bf16 *>(at),
+                         reinterpret_cast<bf16 *>(at + part), round8(F), 0};
+    cudaError_t e = launch_dgate_f32(gate, dp.sm_count, stream);
+    if (e == cudaSuccess && dX) {
+      FewArgs p{};
+      p.M = M;
+      p.N = D;
+      p.K = F;
+      p.rows_are_outputs = op_w == GEMM_OP_N;
+      p.a[0] = dg;
+      p.a[1] = du;
+      p.lda = round8(F);
+      p.b[0] = static_cast<const float *>(Wg);
+      p.b[1] = static_cast<const float *>(Wu);
+      p.ldb[0] = ldwg;
+      p.ldb[1] = ldwu;
+      p.c = static_cast<float *>(dX);
+      p.ldc = lddx;
+      e = launch_few(p, at + 2 * part, dp.sm_count, stream);
+    }
+    if (e == cudaSuccess && dWg) {
+      // stored D x F: rows of X by columns of dG; stored F x D the other way
+      const float *x = static_cast<const float *>(X), *d[2] = {dg, du};
+      OuterArgs p{};
+      p.M = M;
+      p.R = wr;
+      p.N = wc;
+      for (int i = 0; i < 2; ++i) {
+        p.q[i] = op_w == GEMM_OP_N ? x : d[i];
+        p.ldq[i] = op_w == GEMM_OP_N ? ldx : round8(F);
+        p.x[i] = op_w == GEMM_OP_N ? d[i] : x;
+        p.ldx[i] = op_w == GEMM_OP_N ? round8(F) : ldx;
+        p.c[i] = static_cast<float *>(i ? dWu : dWg);
+        p.ldc[i] = i ? lddwu : lddwg;
+      }
+      e = launch_outer(p, stream);
+    }
+    return to_status(e);
+  }
   const uint64_t part = plane_bytes(dtype, M, F);
   uint64_t need = 2 * part;
   if (dX) need += pack_bytes(dtype, wg) + pack_bytes(dtype, wu);

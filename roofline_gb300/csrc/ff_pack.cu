@@ -21,9 +21,8 @@ __device__ __forceinline__ void split3(float x, bf16 (&o)[3]) {
   o[2] = __float2bfloat16_rn(r - __bfloat162float(m));
 }
 
-// Eight values of one row, rounded to P planes, as one 16-byte store each.
 template <int P>
-__device__ __forceinline__ void store8(const float (&v)[8], bf16 *dst, int64_t plane) {
+__device__ __forceinline__ void store_planes(const float (&v)[8], bf16 *dst, int64_t plane) {
   __align__(16) bf16 o[P][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -39,6 +38,19 @@ __device__ __forceinline__ void store8(const float (&v)[8], bf16 *dst, int64_t p
 #pragma unroll
   for (int q = 0; q < P; ++q)
     *reinterpret_cast<uint4 *>(dst + q * plane) = *reinterpret_cast<const uint4 *>(o[q]);
+}
+
+// Eight values of one row, rounded to P planes, as one 16-byte store each; as
+// they are with P = 0 (dst then holds floats).
+template <int P>
+__device__ __forceinline__ void store8(const float (&v)[8], bf16 *dst, int64_t plane) {
+  if constexpr (P == 0) {
+    float4 *to = reinterpret_cast<float4 *>(dst);
+    to[0] = make_float4(v[0], v[1], v[2], v[3]);
+    to[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    store_planes<P>(v, dst, plane);
+  }
 }
 
 // Eight values from column c on (zeros from `cols` on), 16 bytes at a time
@@ -110,9 +122,11 @@ __global__ void __launch_bounds__(256) ff_dgate_kernel(GateAndPack q) {
   const bool vh = rows_aligned(dh, p.lddh), vg = rows_aligned(p.g, p.ldg),
              vu = rows_aligned(p.u, p.ldu);
   for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < all; e += gridDim.x * 256ll) {
-    if (e >= n) {
-      pack_group<T, P>(q.jobs, e - n);
-      continue;
+    if constexpr (P > 0) {
+      if (e >= n) {
+        pack_group<T, P>(q.jobs, e - n);
+        continue;
+      }
     }
     const int64_t r = e / per_row, c = (e - r * per_row) * 8;
     float h[8], g[8], u[8], a[8], d[8];
@@ -128,8 +142,9 @@ __global__ void __launch_bounds__(256) ff_dgate_kernel(GateAndPack q) {
       d[i] = h[i] * u[i] * d[i];
       a[i] = h[i] * a[i];
     }
-    store8<P>(d, p.dg + r * p.ld_out + c, p.plane);
-    store8<P>(a, p.du + r * p.ld_out + c, p.plane);
+    const int64_t to = (r * p.ld_out + c) * (P == 0 ? 2 : 1);  // in bf16
+    store8<P>(d, p.dg + to, p.plane);
+    store8<P>(a, p.du + to, p.plane);
   }
 }
 
@@ -172,6 +187,11 @@ cudaError_t launch_pack(const PackJob *jobs, int n, int dtype, int sms, cudaStre
   const int grid = blocks_for(p.first[p.n], sms);
   if (dtype == GEMM_DT_F32) return launch(ff_pack_kernel<float, 3>, grid, p, s);
   return launch(ff_pack_kernel<bf16, 1>, grid, p, s);
+}
+
+cudaError_t launch_dgate_f32(const DgateArgs &p, int sms, cudaStream_t s) {
+  const GateAndPack q{p, PackJobs{}};
+  return launch(ff_dgate_kernel<float, 0>, blocks_for(p.M * (p.ld_out / 8), sms), q, s);
 }
 
 cudaError_t launch_dgate(const DgateArgs &p, const PackJob *jobs, int n, int dtype, int sms,

@@ -51,7 +51,7 @@ constexpr int kPackJobs = 3;
 cudaError_t launch_pack(const PackJob *jobs, int n, int dtype, int sms, cudaStream_t s);
 
 // dG = dH * U * act'(G) and dU = dH * act(G), M x F (neither 0), as such
-// planes; and the jobs, in the same launch.
+// planes; launch_dgate: and the jobs, in the same launch.
 struct DgateArgs {
   int64_t M, F;
   int act;
@@ -62,6 +62,8 @@ struct DgateArgs {
   bf16 *dg, *du;
   int64_t ld_out, plane;
 };
+// The same as M x ld_out floats at dg and du, from FP32.
+cudaError_t launch_dgate_f32(const DgateArgs &p, int sms, cudaStream_t s);
 cudaError_t launch_dgate(const DgateArgs &p, const PackJob *jobs, int n, int dtype, int sms,
                          cudaStream_t s);
 

@@ -109,6 +109,26 @@ def test_strided_and_misaligned(ff, size, pad, off, dt, order):
     _check_backward(ff, dH, X, Wg, Wu, G, U, "silu")
 
 
+@pytest.mark.parametrize("order", ["oi", "io"])
+@pytest.mark.parametrize("pad", [0, 4, 3])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 7, 8, 9, 13, 16, 17])
+def test_few_tokens_f32(ff, M, pad, order):
+    """Around each number of tokens where FP32's few-token kernels change, with rows and
+    sums that end inside a block's share, aligned and not; the same bits again with a
+    workspace of the stated size."""
+    D, F = (1036, 330) if M % 2 else (270, 1100)
+    X, Wg, Wu, dH = _case(M + pad, M, D, F, F32, order, pad, pad)
+    G, U = _check_forward(ff, X, Wg, Wu, ACTS[M % 4])
+    _check_backward(ff, dH, X, Wg, Wu, G, U, ACTS[M % 4])
+    op = 1 if order == "oi" else 0
+    ws = [torch.empty(max(ff.gated_ff_workspace(M, D, F, ff.DT_F32, op, b), 1),
+                      dtype=torch.uint8, device="cuda") for b in (False, True)]
+    assert torch.equal(ff.gated_ff(X, Wg, Wu, workspace=ws[0]), ff.gated_ff(X, Wg, Wu))
+    for a, b in zip(ff.gated_ff_backward(dH, X, Wg, Wu, G, U, workspace=ws[1]),
+                    ff.gated_ff_backward(dH, X, Wg, Wu, G, U)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("M", [2, 200])
 def test_output_rows_of_wider_buffers_are_left_alone(ff, M, dt):
