@@ -476,8 +476,11 @@ GEMM_API int gemm_f32_splitk_noalloc(int64_t M, int64_t N, int64_t K, float alph
  * (ldw >= D, the "out x in" storage of most model files).
  * dtype: GEMM_DT_F32 or GEMM_DT_BF16, of X, the weights and H.  Products are
  * summed in FP32; act and the product are computed in FP32 from those sums and
- * H is rounded once.  GEMM_DT_F32 has FP32 accuracy.  A non-finite input gives NaN
- * in FP32 (as in GEMM_MODE_TF32X3); in BF16 Inf and NaN follow IEEE rules.
+ * H is rounded once.  GEMM_DT_F32 has FP32 accuracy (for more than a few
+ * tokens a factor is split into three BF16, so what is left of it below
+ * 2^-133 is lost).  A non-finite input gives a non-finite sum: in BF16 by
+ * IEEE rules, in FP32 NaN where IEEE rules would give Inf (as in
+ * GEMM_MODE_TF32X3), but for a few tokens.
  * G, U: the sums for a later backward pass, or both NULL.  They are FP32 in
  * either dtype: rounded to BF16 they would put an error of their own, as
  * large as a BF16 result's rounding, into every gradient.  H may be NULL when
@@ -529,8 +532,10 @@ GEMM_API int gated_ff_workspace(int backward, int dtype, int op_w, int64_t M, in
  * of byte i.  S, Z: N x ceil(K / group) scales and zero points, contiguous,
  * of the same dtype as X and Y; Z may be NULL (every zero point 8).
  * group: 32, 64, 128 or 256.  dtype F32 or BF16; products are summed in
- * FP32 and exact to FP32 in F32.  The weights are read once for every 8
- * tokens (BF16) or 2 (F32): meant for M up to a few dozen.
+ * FP32 and exact to FP32 in F32, where an Inf in X gives NaN.  The weights
+ * are read once for every 16 tokens (BF16) or 4 (F32): meant for M up to a few
+ * dozen, and M up to 262,140 is accepted (GEMM_ERR_UNSUPPORTED beyond).
+ * ldq < 2^32.
  */
 GEMM_API int q4_matmul(int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
                        const void *Q, int64_t ldq, const void *S, const void *Z, int group,
@@ -550,7 +555,8 @@ GEMM_API int q4_gated(int dtype, int act, int64_t M, int64_t N, int64_t K, const
  * grad_norm_clip -- norm = sqrt(sum of all squares) over `count` tensors,
  * and out_i = grad_i * min(1, max_norm / (norm + 1e-6)).
  * grads, outs: HOST arrays of `count` device pointers; sizes: HOST array of
- * element counts (>= 0); dtypes: HOST array of GEMM_DT_*.  The arrays are
+ * element counts (0 to 2^40, and together at most 2^40, else
+ * GEMM_ERR_UNSUPPORTED); dtypes: HOST array of GEMM_DT_*.  The arrays are
  * read before the call returns.  outs == NULL: only the norm.  outs[i] may
  * equal grads[i] (in place); otherwise outputs overlap no input.  Tensors
  * need only be aligned to their element size.

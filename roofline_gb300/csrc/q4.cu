@@ -2,13 +2,20 @@
 // q4_matmul and q4_gated).
 //
 // Y^T = W X^T on mma.sync tiles of 16 weight rows x 8 columns of X^T, BF16 in,
-// FP32 sums.  What bounds it is reading the codes once (N K / 2 bytes), so
-// each thread copies the codes that it alone will use to shared memory ahead
-// of time, asynchronously and a ring of stages deep, and the arithmetic per
-// code is kept under what that leaves: a 32-bit word of eight codes becomes
-// four BF16 pairs 128 + q, exact, by 3 shifts and 4 three-input logic
-// operations that mask and or in the exponent of 128.  The ALU pipe, which
-// runs these at half the issue rate, is what the kernel is nearest to.
+// FP32 sums.  What bounds the product itself is reading the codes once (N K / 2
+// bytes).  So each warp copies its own rows' codes to shared memory ahead of
+// their use, asynchronously, 128 bytes of a row at a time, with no barrier between
+// warps; and the arithmetic per code is kept small: a 32-bit word of eight codes becomes four BF16 pairs
+// 128 + q, exact, by 3 shifts and 4 three-input logic operations that mask and
+// or in the exponent of 128.
+//
+// GB300, from cold caches, BF16, groups of 128: 1 token by 2 x 14336 x 4096
+// (60.6 MB) 20.7 us, 2.9 TB/s, the ALU pipe 50 % and the issue slots 49 %
+// busy: what the codes' conversion costs, with the ramp of a short kernel on
+// both sides.  16 tokens by 8192 x 28672 (132 MB) 59.7 us, 2.2 TB/s: the MMAs'
+// latency and issue with 8 warps an SM.  1 token by 4096 x 4096 (8.7 MB) 6.2
+// us: launch and one pass of latency.
+//
 // Scales multiply the FP32 sums of one group, from which (128 + z) sum x is
 // taken first, with the sums of x from MMAs whose weights are ones; that
 // difference costs about 5 of FP32's 24 bits, which a BF16 result does not
@@ -21,7 +28,8 @@
 // k, W = 1, 2, 4 words each for groups of 32, 64, 128 (or 256).
 //
 // FP32 X is split into three BF16 (24 bits) that take three columns of an MMA
-// each token, so a tile holds 2 tokens, and 8 in BF16.
+// each token, so a tile holds 2 tokens, and 8 in BF16.  4 tokens by 4096 x
+// 14336 take 31 us, 93 when the split rounded each plane.
 //
 // A CTA has one block of rows and its warps split k; their sums meet in shared
 // memory in a fixed order.
@@ -112,7 +120,10 @@ struct Raw8 {
   uint4 v[sizeof(T) / 2];
 };
 
-// The pairs (x_i, x_i+4), i = 0..3, of plane `plane`.
+// The pairs (x_i, x_i+4), i = 0..3, of plane `plane`.  FP32 is cut, not
+// rounded, into its planes, which cannot overflow and takes four operations a
+// value: the first two 8 bits of the fraction with their leading one, the last
+// what is left, 8 bits too.  An Inf leaves NaN in its second and third.
 __device__ __forceinline__ void pairs(const Raw8<bf16> &r, int, uint32_t (&b)[4]) {
   const uint4 v = r.v[0];
   b[0] = __byte_perm(v.x, v.z, 0x5410);
@@ -121,20 +132,16 @@ __device__ __forceinline__ void pairs(const Raw8<bf16> &r, int, uint32_t (&b)[4]
   b[3] = __byte_perm(v.y, v.w, 0x7632);
 }
 __device__ __forceinline__ uint32_t plane_of(float x, int plane) {
-  bf16 h = __float2bfloat16_rn(x);
-  const bool fin = (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
-  if (fin && (__bfloat16_as_ushort(h) & 0x7f80u) == 0x7f80u) h = __float2bfloat16_rz(x);
-  if (plane > 0) {
-    const float r = fin ? x - __bfloat162float(h) : 0.0f;
-    h = __float2bfloat16_rn(r);
-    if (plane > 1) h = __float2bfloat16_rn(r - __bfloat162float(h));
-  }
-  return __bfloat16_as_ushort(h);
+  const uint32_t first = plane > 0 ? 0xffff0000u : 0u, second = plane > 1 ? 0xffff0000u : 0u;
+  x -= __uint_as_float(__float_as_uint(x) & first);
+  x -= __uint_as_float(__float_as_uint(x) & second);
+  return __float_as_uint(x);
 }
 __device__ __forceinline__ void pairs(const Raw8<float> &r, int plane, uint32_t (&b)[4]) {
   const float *f = reinterpret_cast<const float *>(r.v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = plane_of(f[i], plane) | (plane_of(f[i + 4], plane) << 16);
+  for (int i = 0; i < 4; ++i)
+    b[i] = __byte_perm(plane_of(f[i], plane), plane_of(f[i + 4], plane), 0x7632);
 }
 
 // W: words of codes that a thread takes of a row and group (a group is 32 W
@@ -155,8 +162,11 @@ struct Q4Cfg {
   static constexpr int RING = STAGES * SLOT, RED = TI * 16 * COLS * 4;
   static constexpr int WARP_BYTES = RING > RED ? RING : RED;
   // Warps that an SM holds.  With four tiles 8 run faster than 12 (16 x 8192 x
-  // 28672: 68 against 78 us): what shared memory they leave is L1 for x.
-  static constexpr int BY_SMEM = 226 * 1024 / WARP_BYTES, BY_REGS = TI == 4 ? 8 : 16;
+  // 28672: 68 against 78 us): what shared memory they leave is L1 for x.  With
+  // two and two of columns of large groups 12, by their registers (16 x 2048 x
+  // 8192: 12.4 us, with 16 warps 16.5).
+  static constexpr int BY_SMEM = 226 * 1024 / WARP_BYTES,
+                       BY_REGS = TI == 4 ? 8 : NT == 2 && W == 4 ? 12 : 16;
   static constexpr int SM_WARPS = BY_SMEM < BY_REGS ? BY_SMEM / 4 * 4 : BY_REGS;
   static constexpr int MAX_WARPS = SM_WARPS < kMaxWarps ? SM_WARPS : kMaxWarps;
 };
@@ -466,8 +476,11 @@ cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, const DeviceProps &dp) {
   return cudaGetLastError();
 }
 
-// Two tiles for one tile of columns; four for two, whose x is then loaded
-// half as often.
+// One tile of columns: two tiles of rows.  Two tiles of columns: four, which
+// load x half as often, where they are faster: a block of four takes about 20/13
+// of a block of two, and an SM runs one of either at a time.  GB300, 16
+// tokens, us with two / four: 4096 x 4096 10.3 / 12.4, 1341 x 2050 11 / 22.6,
+// 5000 x 4096 20.5 / 14.3, 8192 x 28672 82 / 59.7, 2 x 5504 x 4096 23.8 / 30.8.
 template <typename T, int W, bool GATED>
 cudaError_t pick_tiles(Q4Args p, cudaStream_t s, const DeviceProps &dp) {
   constexpr int parts = 8 / W, bytes = parts * (int)sizeof(T) < 16 ? parts * (int)sizeof(T) : 16;
@@ -478,8 +491,12 @@ cudaError_t pick_tiles(Q4Args p, cudaStream_t s, const DeviceProps &dp) {
   }
   p.aligned = q % 16 == 0;
   p.scales_aligned = p.group == 32 * W && sc % bytes == 0 && bytes >= 4;
-  return p.M > kTileTokens<T> ? launch_q4<T, W, 4, 2, GATED>(p, s, dp)
-                              : launch_q4<T, W, 2, 1, GATED>(p, s, dp);
+  if (p.M <= kTileTokens<T>) return launch_q4<T, W, 2, 1, GATED>(p, s, dp);
+  const int64_t passes = ceil_div(p.M, kTileTokens<T> * 2);
+  auto waves = [&](int rows) { return ceil_div(ceil_div(p.N, rows) * passes, dp.sm_count); };
+  return 13 * waves(GATED ? 16 : 32) < 20 * waves(GATED ? 32 : 64)
+             ? launch_q4<T, W, 2, 2, GATED>(p, s, dp)
+             : launch_q4<T, W, 4, 2, GATED>(p, s, dp);
 }
 
 template <typename T, bool GATED>
