@@ -815,54 +815,45 @@ Choice choice_of(const FfProduct &q, int cg, int bn) {
 }
 
 // The tiles of n products (one, or two of one launch) with the least
-// estimated time: whole waves of one product's tiles, or all tiles spread
-// evenly and one more of the second product; and for a CTA's last tile an
-// epilogue that nothing hides, about 30 clocks a column.  Two products share
-// the CTAs of a tile, and with three planes the kernel's columns.
+// estimated time.  One product: whole waves of its tiles and an epilogue that
+// nothing hides, about 30 clocks a column.  Two, whose tiles are one list:
+// all work spread evenly and one more tile of the second product, but no less
+// than the first one's waves.  Two products share the CTAs of a tile, and
+// with three planes the kernel's columns.
 void choose(const FfProduct *q, int n, int sms, Choice *best) {
+  struct Candidate {
+    Choice c;
+    double clocks, waves, even;  // of a tile; of all tiles, whole and spread
+  };
   double least = 0.0;
   for (int cg = 2; cg >= 1; --cg) {
-    const double workers = sms / cg;
-    if (n == 1 || q[0].planes == 3) {
+    const int64_t workers = sms / cg;
+    Candidate list[2][16];
+    int count[2] = {0, 0};
+    for (int i = 0; i < n; ++i)
       for (int bn = 256; bn >= 32; bn -= 16) {
-        if (!tile_fits(q[0], cg, bn) || (n == 2 && !tile_fits(q[1], cg, bn))) continue;
-        Choice c[2];
-        double t = 30.0 * bn, all = 0.0, clocks = 0.0;
-        for (int i = 0; i < n; ++i) {
-          c[i] = choice_of(q[i], cg, bn);
-          clocks = tile_clocks(q[i], c[i]);
-          const double tiles = (double)tiles_of(q[i], c[i]);
-          all += clocks * (n == 1 ? (double)ceil_div((int64_t)tiles, (int64_t)workers) : tiles / workers);
+        if (!tile_fits(q[i], cg, bn)) continue;
+        const Choice c = choice_of(q[i], cg, bn);
+        const double clocks = tile_clocks(q[i], c);
+        const int64_t tiles = tiles_of(q[i], c);
+        list[i][count[i]++] = {c, clocks, clocks * (double)ceil_div(tiles, workers),
+                               clocks * (double)tiles / (double)workers};
+      }
+    for (int i = 0; i < count[0]; ++i) {
+      const Candidate &x = list[0][i];
+      for (int j = 0; j < (n == 2 ? count[1] : 1); ++j) {
+        double t = x.waves + 30.0 * x.c.bn;
+        if (n == 2) {
+          const Candidate &y = list[1][j];
+          if (q[0].planes == 3 && x.c.bn != y.c.bn) continue;
+          const double even = x.even + y.even + y.clocks + 15.0 * (x.c.bn + y.c.bn);
+          if (even > t) t = even;
         }
-        t += all + (n == 2 ? clocks : 0.0);
         if (least == 0.0 || t < least) {
           least = t;
-          for (int i = 0; i < n; ++i) best[i] = c[i];
+          best[0] = x.c;
+          if (n == 2) best[1] = list[1][j].c;
         }
-      }
-    } else {
-      // each product's width by itself: what it adds to every worker's time
-      Choice c[2];
-      double t = 0.0;
-      for (int i = 0; i < 2; ++i) {
-        double part = 0.0;
-        for (int bn = 256; bn >= 32; bn -= 16) {
-          if (!tile_fits(q[i], cg, bn)) continue;
-          const Choice x = choice_of(q[i], cg, bn);
-          const double clocks = tile_clocks(q[i], x);
-          const double v = clocks * (double)tiles_of(q[i], x) / workers + (i == 1 ? clocks : 0.0) +
-                           15.0 * bn;
-          if (part == 0.0 || v < part) {
-            part = v;
-            c[i] = x;
-          }
-        }
-        t += part;
-      }
-      if (least == 0.0 || t < least) {
-        least = t;
-        best[0] = c[0];
-        best[1] = c[1];
       }
     }
   }
@@ -894,7 +885,11 @@ int launch_cfg(const FfProduct *q, int n, const Choice *ch, const DeviceProps &d
   if (workers > tiles) workers = tiles;
   l.stages = kStageBudget / l.stage_bytes < kMaxStages ? kStageBudget / l.stage_bytes : kMaxStages;
   l.early_from = l.p[0].tiles % workers;
-  l.early = n == 2 && l.early_from > 0 ? (int64_t)(clocks[0] / clocks[1]) : 0;
+  if (n == 2 && l.early_from > 0) {
+    const int64_t share = ceil_div(l.p[1].tiles, workers - l.early_from);
+    l.early = (int64_t)(clocks[0] / clocks[1]);
+    if (l.early > share) l.early = share;
+  }
   l.wait_ns = env_u64("GEMM_DEBUG_WAIT_LIMIT_NS", 2000000000ull);
   l.stall_producer = (int)env_u64("GEMM_DEBUG_STALL_PRODUCER", 0);
 
