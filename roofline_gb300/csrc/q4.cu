@@ -65,6 +65,11 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, int byte
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+// The first `bytes` of 16, zeros for the rest.
+__device__ __forceinline__ void cp_async_part(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -157,6 +162,8 @@ struct Q4Cfg {
   static constexpr int STAGES = 2;
   static constexpr int SCALES = TI * 16 * PARTS * (int)sizeof(T);  // bytes, one stage
   static constexpr int SLOT = TI * 16 * 128 + 2 * SCALES;          // codes, scales, zero points
+  // unaligned rows: one 16-byte piece more of each, behind all the rings
+  static constexpr int TAIL = TI * 16 * 16, WARP_TAILS = STAGES * TAIL;
   static_assert(!GATED || TI % 2 == 0, "");
   // the ring of a warp, or its share of the sums
   static constexpr int RING = STAGES * SLOT, RED = TI * 16 * COLS * 4;
@@ -183,6 +190,7 @@ q4_kernel(const Q4Args p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warps = blockDim.x >> 5;
   uint8_t *ring = shared + warp * Cfg::WARP_BYTES;
+  uint8_t *tails = shared + warps * Cfg::WARP_BYTES + warp * Cfg::WARP_TAILS;
   const bool has_z = p.w[0].z != nullptr;
   const uint32_t mask = p.mask;
   const int64_t m0 = (int64_t)blockIdx.y * (kTileTokens<T> * NT);
@@ -210,7 +218,7 @@ q4_kernel(const Q4Args p) {
 
   // Step `c`'s codes, scales and zero points of all the warp's rows, to slot `st`.
   auto copy = [&](int c, int st) {
-    uint8_t *slot = ring + st * Cfg::SLOT;
+    uint8_t *slot = ring + st * Cfg::SLOT, *tail = tails + st * Cfg::TAIL;
     const int64_t at = (int64_t)c * (STEP / 2);
     auto source = [&](int i) {  // of rows 4 i on
       const int k = i * 4 / ROWS, r = i * 4 % ROWS + lr;
@@ -221,33 +229,32 @@ q4_kernel(const Q4Args p) {
 #pragma unroll
       for (int i = 0; i < RW / 4; ++i) cp_async(dst + to[i & 1] + i * 512, source(i), 16);
     } else {
-      // unaligned rows, and the ends of the rows: the aligned words that hold
-      // the piece, shifted; code 8 beyond the matrix
-#pragma unroll 1
+      // unaligned rows, and the ends of the rows: the aligned 16 bytes that a
+      // piece begins in (realign() shifts them), without what lies outside the
+      // matrix; x is zero where the codes then are
+      auto fetch = [&](int k, uint8_t *to_byte, const uint8_t *src) {
+        const uint8_t *first = p.w[k].q, *end = first + (p.N - 1) * p.w[k].ldq + row_bytes;
+        if (src >= first) {
+          const int64_t bytes = end - src;
+          if (bytes <= 0) src = end - 1 - (reinterpret_cast<uintptr_t>(end - 1) & 15);
+          cp_async_part((uint32_t)__cvta_generic_to_shared(to_byte), src,
+                        bytes >= 16 ? 16 : bytes > 0 ? (int)bytes : 0);
+        } else {
+          for (int b = 0; b < 16; ++b)
+            to_byte[b] = src + b >= first && src + b < end ? src[b] : (uint8_t)0;
+        }
+      };
+#pragma unroll 4
       for (int i = 0; i < RW / 4; ++i) {
         const uint8_t *src = source(i);
-        const Q4Side &w = p.w[i * 4 / ROWS];
-        const uint8_t *first = w.q, *end = first + (p.N - 1) * w.ldq + row_bytes;
-        const int off = (int)(reinterpret_cast<uintptr_t>(src) & 3);
-        src -= off;
-        uint32_t v[5];
-        if (src >= first && src + 20 <= end) {
+        fetch(i * 4 / ROWS, slot + i * 512 + to[i & 1], src - (reinterpret_cast<uintptr_t>(src) & 15));
+      }
 #pragma unroll
-          for (int j = 0; j < 5; ++j) v[j] = __ldg(reinterpret_cast<const uint32_t *>(src) + j);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 5; ++j) {
-            v[j] = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint8_t *q = src + 4 * j + b;
-              v[j] |= (uint32_t)(q >= first && q < end ? *q : 0x88) << (8 * b);
-            }
-          }
-        }
-        *reinterpret_cast<uint4 *>(slot + (i & 1 ? to[1] : to[0]) + i * 512) =
-            make_uint4(__funnelshift_r(v[0], v[1], 8 * off), __funnelshift_r(v[1], v[2], 8 * off),
-                       __funnelshift_r(v[2], v[3], 8 * off), __funnelshift_r(v[3], v[4], 8 * off));
+      for (int i = 0; i < RW; i += 32) {
+        const int e = i + lane, k = e / ROWS, r = e % ROWS;
+        const uint8_t *src = p.w[k].q + at + weight_row(r) * p.w[k].ldq;
+        const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+        if (off) fetch(k, tail + e * 16, src - off + 128);
       }
     }
     // scales and zero points: PARTS a row, in the order of k
@@ -268,18 +275,54 @@ q4_kernel(const Q4Args p) {
                    static_cast<const T *>(w.z) + from, PIECE);
       }
     } else {
+      // four loads at a time, then their stores: one wait for all four
+      auto gather = [&](bool zero, T *dst) {
+        constexpr int EACH = RW * PARTS / 32, AT_ONCE = EACH < 4 ? EACH : 4;
 #pragma unroll 1
-      for (int e = lane; e < RW * PARTS; e += 32) {
-        const int r = e / PARTS, k = r / ROWS;
-        const Q4Side &w = p.w[GATED ? k : 0];
-        const int64_t gr = ((int64_t)c * STEP + e % PARTS * (32 * W)) >> p.group_shift;
-        const int64_t from = weight_row(r - k * ROWS) * p.groups + gr;
-        ds[e] = gr < p.groups ? static_cast<const T *>(w.s)[from] : from_f32<T>(0.0f);
-        if (has_z)
-          ds[RW * PARTS + e] = gr < p.groups ? static_cast<const T *>(w.z)[from]
-                                             : from_f32<T>(0.0f);
-      }
+        for (int i = 0; i < EACH; i += AT_ONCE) {
+          T v[AT_ONCE];
+#pragma unroll
+          for (int j = 0; j < AT_ONCE; ++j) {
+            const int e = (i + j) * 32 + lane, r = e / PARTS, k = r / ROWS;
+            const int64_t gr = ((int64_t)c * STEP + e % PARTS * (32 * W)) >> p.group_shift;
+            const Q4Side &w = p.w[GATED ? k : 0];
+            const T *from = static_cast<const T *>(zero ? w.z : w.s);
+            v[j] = gr < p.groups ? from[weight_row(r - k * ROWS) * p.groups + gr] : from_f32<T>(0.0f);
+          }
+#pragma unroll
+          for (int j = 0; j < AT_ONCE; ++j) dst[(i + j) * 32 + lane] = v[j];
+        }
+      };
+      gather(false, ds);
+      if (has_z) gather(true, ds + RW * PARTS);
     }
+  };
+  // Shifts the rows of a slot to where aligned ones lie: a row's codes begin
+  // its address's last four bits into its first piece, in every step alike.
+  auto realign = [&](int st) {
+    uint8_t *slot = ring + st * Cfg::SLOT;
+    const uint8_t *tail = tails + st * Cfg::TAIL;
+#pragma unroll 2
+    for (int i = 0; i < RW / 4; ++i) {
+      const int k = i * 4 / ROWS, r = i * 4 % ROWS + lr, e = i * 4 + lr;
+      const uint32_t off = ((uint32_t)reinterpret_cast<uintptr_t>(p.w[k].q) +
+                            (uint32_t)weight_row(r) * (uint32_t)p.w[k].ldq) & 15;
+      uint4 *here = reinterpret_cast<uint4 *>(slot + i * 512 + to[i & 1]);
+      const uint4 a = *here;
+      const uint4 b = *reinterpret_cast<const uint4 *>(
+          lc < 7 ? slot + piece(e, lc + 1) : tail + e * 16);
+      uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 6; ++j) v[j] = off & 8 ? v[j + 2] : v[j];
+#pragma unroll
+      for (int j = 0; j < 5; ++j) v[j] = off & 4 ? v[j + 1] : v[j];
+      __syncwarp();
+      *here = make_uint4(__funnelshift_r(v[0], v[1], 8 * (off & 3)),
+                         __funnelshift_r(v[1], v[2], 8 * (off & 3)),
+                         __funnelshift_r(v[2], v[3], 8 * (off & 3)),
+                         __funnelshift_r(v[3], v[4], 8 * (off & 3)));
+    }
+    __syncwarp();
   };
 
   // This lane's column of each tile of X^T.  A column without a token stands
@@ -341,6 +384,7 @@ q4_kernel(const Q4Args p) {
     if (it + STAGES - 1 < mine) copy(c + (STAGES - 1) * warps, (it + STAGES - 1) % STAGES);
     cp_async_commit();
     const uint8_t *slot = ring + st * Cfg::SLOT;
+    if (!p.aligned) realign(st);
     const T *ds = reinterpret_cast<const T *>(slot + RW * 128);
 #pragma unroll 1
     for (int part = 0; part < PARTS; ++part) {
@@ -461,10 +505,11 @@ q4_kernel(const Q4Args p) {
 template <typename T, int W, int TI, int NT, bool GATED>
 cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, const DeviceProps &dp) {
   using Cfg = Q4Cfg<T, W, TI, NT, GATED>;
-  static_assert(Cfg::WARP_BYTES * Cfg::MAX_WARPS <= 227 * 1024 && Cfg::MAX_WARPS >= 4, "");
+  constexpr int MOST = (Cfg::WARP_BYTES + Cfg::WARP_TAILS) * Cfg::MAX_WARPS;
+  static_assert(MOST <= 227 * 1024 && Cfg::MAX_WARPS >= 4, "");
   auto kern = q4_kernel<T, W, TI, NT, GATED>;
   static Once once;
-  const cudaError_t e = allow_shared_memory(once, kern, Cfg::WARP_BYTES * Cfg::MAX_WARPS, dp.device);
+  const cudaError_t e = allow_shared_memory(once, kern, MOST, dp.device);
   if (e != cudaSuccess) return e;
   // Warps: as many as fill the SMs, but no more than there are steps.
   const int64_t ctas = ceil_div(p.N, Cfg::ROWS), steps = ceil_div(p.K, Cfg::STEP);
@@ -472,7 +517,7 @@ cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, const DeviceProps &dp) {
   warps = warps < 4 ? 4 : warps > Cfg::MAX_WARPS ? Cfg::MAX_WARPS : warps;
   if (warps > steps) warps = steps < 1 ? 1 : steps;
   kern<<<dim3((unsigned)ctas, (unsigned)ceil_div(p.M, kTileTokens<T> * NT)), (unsigned)warps * 32,
-         Cfg::WARP_BYTES * warps, s>>>(p);
+         (Cfg::WARP_BYTES + (p.aligned ? 0 : Cfg::WARP_TAILS)) * warps, s>>>(p);
   return cudaGetLastError();
 }
 
