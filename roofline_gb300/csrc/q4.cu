@@ -32,7 +32,13 @@
 // 14336 take 31 us, 93 when the split rounded each plane.
 //
 // A CTA has one block of rows and its warps split k; their sums meet in shared
-// memory in a fixed order.
+// memory in a fixed order.  Where the blocks of rows are few and long, a
+// cluster of up to 8 CTAs shares one, and reads one another's sums: 1 token by
+// 512 x 16384 8.3 us, 14.4 with one CTA a block.
+//
+// Rows that do not start on 16-byte boundaries are copied by the aligned
+// pieces that they lie in and shifted in shared memory (3 tokens by 2 x 758 x
+// 21645, group 32: 37 us; 82 with loads through registers and no clusters).
 #include "ff.cuh"
 
 namespace gg {
@@ -53,6 +59,7 @@ struct Q4Args {
   int group_shift;  // group = 1 << group_shift
   int vec_x;        // rows of X start on 16-byte boundaries
   int aligned, scales_aligned;  // rows of codes on 16 bytes; a step's scales on theirs
+  int split;                    // CTAs (a cluster) that share a block of rows, each a part of k
 };
 
 constexpr int kMaxWarps = 16;  // of a CTA: its parts of k
@@ -76,6 +83,31 @@ __device__ __forceinline__ void cp_async_commit() {
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Of a launch without clusters: 0 and blockIdx.x.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_id() {
+  uint32_t r;
+  asm("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;" ::: "memory");
+}
+// A float of the shared memory of the cluster's CTA `rank`, at `p` in this one's.
+__device__ __forceinline__ float load_of(const float *p, uint32_t rank) {
+  float v;
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n"
+               " ld.shared::cluster.f32 %0, [a];\n}"
+               : "=f"(v)
+               : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank)
+               : "memory");
+  return v;
 }
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -171,9 +203,10 @@ struct Q4Cfg {
   // Warps that an SM holds.  With four tiles 8 run faster than 12 (16 x 8192 x
   // 28672: 68 against 78 us): what shared memory they leave is L1 for x.  With
   // two and two of columns of large groups 12, by their registers (16 x 2048 x
-  // 8192: 12.4 us, with 16 warps 16.5).
+  // 8192: 12.4 us, with 16 warps 16.5), and 8 in FP32 (4 x 4096 x 14336: 28.7
+  // us, with 12 32.7).
   static constexpr int BY_SMEM = 226 * 1024 / WARP_BYTES,
-                       BY_REGS = TI == 4 ? 8 : NT == 2 && W == 4 ? 12 : 16;
+                       BY_REGS = TI == 4 ? 8 : NT == 2 && W == 4 ? (sizeof(T) == 4 ? 8 : 12) : 16;
   static constexpr int SM_WARPS = BY_SMEM < BY_REGS ? BY_SMEM / 4 * 4 : BY_REGS;
   static constexpr int MAX_WARPS = SM_WARPS < kMaxWarps ? SM_WARPS : kMaxWarps;
 };
@@ -188,16 +221,17 @@ q4_kernel(const Q4Args p) {
   extern __shared__ __align__(128) uint8_t shared[];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int warps = blockDim.x >> 5;
+  const int warps = blockDim.x >> 5, rank = (int)cluster_rank();
+  const int part_of_k = rank * warps + warp, parts_of_k = p.split * warps;
   uint8_t *ring = shared + warp * Cfg::WARP_BYTES;
   uint8_t *tails = shared + warps * Cfg::WARP_BYTES + warp * Cfg::WARP_TAILS;
   const bool has_z = p.w[0].z != nullptr;
   const uint32_t mask = p.mask;
   const int64_t m0 = (int64_t)blockIdx.y * (kTileTokens<T> * NT);
-  const int64_t n0 = (int64_t)blockIdx.x * ROWS;
+  const int64_t n0 = (int64_t)cluster_id() * ROWS;
   const int left = (int)(p.N - n0 < ROWS ? p.N - n0 : ROWS);
   const int steps = (int)((p.K + STEP - 1) / STEP);
-  const int mine = steps > warp ? (steps - warp + warps - 1) / warps : 0;
+  const int mine = steps > part_of_k ? (steps - part_of_k + parts_of_k - 1) / parts_of_k : 0;
   const int64_t row_bytes = (p.K + 1) / 2;
   // Rows that the matrix does not have stand for its last one: what is
   // computed of them is not stored.
@@ -364,7 +398,7 @@ q4_kernel(const Q4Args p) {
 
 #pragma unroll 1
   for (int st = 0; st < STAGES - 1; ++st) {
-    if (st < mine) copy(warp + st * warps, st);
+    if (st < mine) copy(part_of_k + st * parts_of_k, st);
     cp_async_commit();
   }
   float acc[TI][NT][4];
@@ -375,13 +409,13 @@ q4_kernel(const Q4Args p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.0f;
 
-  if (mine > 0) fetch_x((int64_t)warp * STEP);
+  if (mine > 0) fetch_x((int64_t)part_of_k * STEP);
 #pragma unroll 1
   for (int it = 0; it < mine; ++it) {
-    const int c = warp + it * warps, st = it % STAGES;
+    const int c = part_of_k + it * parts_of_k, st = it % STAGES;
     cp_async_wait<STAGES - 2>();
     __syncwarp();  // this step is here, and every lane is done with the one before
-    if (it + STAGES - 1 < mine) copy(c + (STAGES - 1) * warps, (it + STAGES - 1) % STAGES);
+    if (it + STAGES - 1 < mine) copy(c + (STAGES - 1) * parts_of_k, (it + STAGES - 1) % STAGES);
     cp_async_commit();
     const uint8_t *slot = ring + st * Cfg::SLOT;
     if (!p.aligned) realign(st);
@@ -396,7 +430,7 @@ q4_kernel(const Q4Args p) {
       if (part + 1 < PARTS)
         fetch_x((int64_t)c * STEP + (part + 1) * (32 * W));
       else if (it + 1 < mine)
-        fetch_x((int64_t)(c + warps) * STEP);
+        fetch_x((int64_t)(c + parts_of_k) * STEP);
       float xs[NT][4];
       if (!EXACT || has_z) {
         constexpr uint32_t one = 0x3f803f80u;
@@ -478,6 +512,16 @@ q4_kernel(const Q4Args p) {
         *reinterpret_cast<float2 *>(red + ((warp * TI + i) * 16 + 8 * h + g) * COLS + nt * 8 +
                                     2 * t) = make_float2(acc[i][nt][2 * h], acc[i][nt][2 * h + 1]);
   __syncthreads();
+  if (p.split > 1) {
+    // this CTA's sums, in place of its first warp's, for the cluster to read
+    for (int e = tid; e < RW * COLS; e += blockDim.x) {
+      float v = 0.0f;
+#pragma unroll 4
+      for (int w = 0; w < warps; ++w) v += red[w * RW * COLS + e];
+      red[e] = v;
+    }
+    cluster_sync();
+  }
   constexpr int TOKENS = kTileTokens<T> * NT;
   auto total = [&](int r, int m) {
     float v = 0.0f;
@@ -485,12 +529,16 @@ q4_kernel(const Q4Args p) {
     const int col = m / kTileTokens<T> * 8 + m % kTileTokens<T> * PLANES;
 #pragma unroll
     for (int q = PLANES - 1; q >= 0; --q)
+      if (p.split > 1) {
+        for (int cta = 0; cta < p.split; ++cta) v += load_of(red + r * COLS + col + q, cta);
+      } else {
 #pragma unroll 4
-      for (int w = 0; w < warps; ++w) v += red[(w * RW + r) * COLS + col + q];
+        for (int w = 0; w < warps; ++w) v += red[(w * RW + r) * COLS + col + q];
+      }
     return v;
   };
   const int tokens = (int)(p.M - m0 < TOKENS ? p.M - m0 : TOKENS);
-  for (int e = tid; e < ROWS * tokens; e += blockDim.x) {
+  for (int e = rank * blockDim.x + tid; e < ROWS * tokens; e += p.split * blockDim.x) {
     const int r = e % ROWS, m = e / ROWS;
     if (r >= left) continue;
     float y = total(r, m);
@@ -500,10 +548,11 @@ q4_kernel(const Q4Args p) {
     }
     static_cast<T *>(p.y)[(m0 + m) * p.ldy + n0 + r] = from_f32<T>(y);
   }
+  if (p.split > 1) cluster_sync();  // the others have read this CTA's sums
 }
 
 template <typename T, int W, int TI, int NT, bool GATED>
-cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, const DeviceProps &dp) {
+cudaError_t launch_q4(Q4Args p, cudaStream_t s, const DeviceProps &dp) {
   using Cfg = Q4Cfg<T, W, TI, NT, GATED>;
   constexpr int MOST = (Cfg::WARP_BYTES + Cfg::WARP_TAILS) * Cfg::MAX_WARPS;
   static_assert(MOST <= 227 * 1024 && Cfg::MAX_WARPS >= 4, "");
@@ -511,14 +560,29 @@ cudaError_t launch_q4(const Q4Args &p, cudaStream_t s, const DeviceProps &dp) {
   static Once once;
   const cudaError_t e = allow_shared_memory(once, kern, MOST, dp.device);
   if (e != cudaSuccess) return e;
-  // Warps: as many as fill the SMs, but no more than there are steps.
+  // Warps: as many as fill the SMs, but no more than there are steps.  Blocks
+  // of rows that leave SMs idle are split along k, while that gives a warp
+  // fewer steps.
+  const int64_t passes = ceil_div(p.M, kTileTokens<T> * NT);
   const int64_t ctas = ceil_div(p.N, Cfg::ROWS), steps = ceil_div(p.K, Cfg::STEP);
   int64_t warps = (int64_t)Cfg::SM_WARPS * dp.sm_count / ctas;
   warps = warps < 4 ? 4 : warps > Cfg::MAX_WARPS ? Cfg::MAX_WARPS : warps;
-  if (warps > steps) warps = steps < 1 ? 1 : steps;
-  kern<<<dim3((unsigned)ctas, (unsigned)ceil_div(p.M, kTileTokens<T> * NT)), (unsigned)warps * 32,
-         (Cfg::WARP_BYTES + (p.aligned ? 0 : Cfg::WARP_TAILS)) * warps, s>>>(p);
-  return cudaGetLastError();
+  int split = 1;
+  while (split < 8 && 2 * split * ctas * passes <= dp.sm_count && steps > split * warps) split *= 2;
+  if (warps * split > steps) warps = steps < 1 ? 1 : ceil_div(steps, split);
+  p.split = split;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(ctas * split), (unsigned)passes);
+  lc.blockDim = dim3((unsigned)warps * 32);
+  lc.dynamicSmemBytes = (Cfg::WARP_BYTES + (p.aligned ? 0 : Cfg::WARP_TAILS)) * warps;
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = split > 1;
+  return cudaLaunchKernelEx(&lc, kern, p);
 }
 
 // One tile of columns: two tiles of rows.  Two tiles of columns: four, which

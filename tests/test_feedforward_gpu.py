@@ -326,6 +326,24 @@ def test_q4(ff, size, dt, zeros, group):
 
 
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M", [1, 3, 16, 19])
+@pytest.mark.parametrize("N,K", [(5, 20000), (33, 12345), (200, 8192), (1000, 8200), (3000, 4104)])
+def test_q4_few_rows_long_sums(ff, N, K, M, dt):
+    """Blocks of rows whose sums several thread blocks share, each a part that need not
+    be whole steps; equal calls give equal bits."""
+    g = torch.Generator().manual_seed(N + M)
+    X = _mat(g, M, K, dt)
+    w, u = _quant(g, N, K, 64, dt, True), _quant(g, N, K, 64, dt, True)
+    Y = ff.q4_matmul(X, w[0], w[1], zeros=w[2], group=64)
+    H = ff.q4_gated(X, w[0], w[1], u[0], u[1], zeros_g=w[2], zeros_u=u[2], group=64, act="silu")
+    again = ff.q4_matmul(X, w[0], w[1], zeros=w[2], group=64)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, again)
+    assert ref.worst(Y, ref.q4_rounded(X, *w, 64)) <= 1.0
+    assert ref.worst(H, ref.q4_gated(X, w, u, 64, "silu")) <= 1.0
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("pad,off", [(0, 1), (1, 0), (3, 1), (16, 0), (15, 5)])
 @pytest.mark.parametrize("K", [96, 513])
 def test_q4_strides(ff, K, pad, off, dt):
