@@ -12,8 +12,9 @@
 // GB300, from cold caches, BF16, groups of 128: 1 token by 2 x 14336 x 4096
 // (60.6 MB) 20.7 us, 2.9 TB/s, the ALU pipe 50 % and the issue slots 49 %
 // busy: what the codes' conversion costs, with the ramp of a short kernel on
-// both sides.  16 tokens by 8192 x 28672 (132 MB) 59.7 us, 2.2 TB/s: the MMAs'
-// latency and issue with 8 warps an SM.  1 token by 4096 x 4096 (8.7 MB) 6.2
+// both sides.  16 tokens by 8192 x 28672 (132 MB) 61.5 us, 2.1 TB/s: without
+// the copies 49, without x's loads 55, the copies alone 29; the arithmetic is
+// no faster with 16 warps (MMA and ALU work add up).  1 token by 4096 x 4096 (8.7 MB) 6.2
 // us: launch and one pass of latency.
 //
 // Scales multiply the FP32 sums of one group, from which (128 + z) sum x is
@@ -589,7 +590,7 @@ cudaError_t launch_q4(Q4Args p, cudaStream_t s, const DeviceProps &dp) {
 // load x half as often, where they are faster: a block of four takes about 20/13
 // of a block of two, and an SM runs one of either at a time.  GB300, 16
 // tokens, us with two / four: 4096 x 4096 10.3 / 12.4, 1341 x 2050 11 / 22.6,
-// 5000 x 4096 20.5 / 14.3, 8192 x 28672 82 / 59.7, 2 x 5504 x 4096 23.8 / 30.8.
+// 5000 x 4096 20.5 / 14.3, 8192 x 28672 82 / 61.5, 2 x 5504 x 4096 23.8 / 30.8.
 template <typename T, int W, bool GATED>
 cudaError_t pick_tiles(Q4Args p, cudaStream_t s, const DeviceProps &dp) {
   constexpr int parts = 8 / W, bytes = parts * (int)sizeof(T) < 16 ? parts * (int)sizeof(T) : 16;
