@@ -12,6 +12,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <climits>
 #include <stdexcept>
 #include <string>
 #include <vector>
@@ -45,6 +46,22 @@ void check(const Tensor &t, const char *name, int64_t rows, int64_t cols, at::Sc
   if (!t.is_cuda() || t.get_device() != device)
     refuse(std::string(name) + " must be on CUDA device " + std::to_string(device));
 }
+
+// An integer argument from lo to hi; refused, not narrowed, beyond them: the
+// library takes ints, and a matrix's width is checked for this very value.
+int64_t integer(PyObject *o, const char *name, int64_t lo, int64_t hi) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be an integer of 64 bits at most");
+  }
+  if (v < lo || v > hi)
+    refuse(std::string(name) + " must be from " + std::to_string(lo) + " to " + std::to_string(hi));
+  return v;
+}
+// Which activations and groups there are the library says itself.
+int act_of(PyObject *o) { return (int)integer(o, "act", INT_MIN, INT_MAX); }
+int64_t group_of(PyObject *o) { return integer(o, "group", 1, INT_MAX); }
 
 // Leading dimension of a row-major matrix.  The row stride of a one-row
 // matrix is never used.
@@ -139,7 +156,7 @@ PyObject *gated_ff_(PyObject *const *a) {
   check(wg, "Wg", D, F, x.type, x.device);
   check(wu, "Wu", D, F, x.type, x.device);
   const Weight g(wg, "Wg"), u(wu, "Wu");
-  const int op = common_op(g, u), act = (int)PyLong_AsLong(a[3]);
+  const int op = common_op(g, u), act = act_of(a[3]);
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.device);
   Tensor H, G, U;
   int64_t ldh = positive(F);
@@ -179,7 +196,7 @@ PyObject *gated_ff_backward_(PyObject *const *a) {
   check(G, "G", M, F, at::kFloat, x.device);
   check(U, "U", M, F, at::kFloat, x.device);
   const Weight g(wg, "Wg"), u(wu, "Wu");
-  const int op = common_op(g, u), act = (int)PyLong_AsLong(a[6]);
+  const int op = common_op(g, u), act = act_of(a[6]);
   const int64_t ldh = leading(dh, "dH"), ldg = leading(G, "G"), ldu = leading(U, "U");
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.device);
   Tensor dX, dWg, dWu;
@@ -228,11 +245,6 @@ struct Quantised {
   }
 };
 
-int64_t group_of(PyObject *o) {
-  const int64_t g = PyLong_AsLongLong(o);
-  if (g <= 0) refuse("group must be positive");
-  return g;
-}
 int64_t rows_of(PyObject *o, const char *name) {
   const Tensor &t = tensor(o, name);
   if (t.dim() != 2) refuse(std::string(name) + " must be a 2-D tensor");
@@ -267,7 +279,7 @@ PyObject *q4_gated_(PyObject *const *a) {
   const First x(a[0], "X");
   const int64_t group = group_of(a[7]), N = rows_of(a[1], "Wq_g");
   const Quantised g(a[1], a[2], a[3], N, x, group, "Wq_g"), u(a[4], a[5], a[6], N, x, group, "Wq_u");
-  const int act = (int)PyLong_AsLong(a[8]);
+  const int act = act_of(a[8]);
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.device);
   Tensor H;
   int64_t ldh = positive(N);
@@ -314,6 +326,10 @@ PyObject *grad_norm_clip_(PyObject *const *a) {
     out[i] = o.data_ptr();
   }
   const double max_norm = PyFloat_AsDouble(a[2]);
+  if (max_norm == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse("max_norm must be a number");
+  }
   if (device < 0) device = c10::cuda::current_device();
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
   Tensor norm = at::empty({}, at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, device));

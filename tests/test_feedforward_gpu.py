@@ -536,3 +536,33 @@ def test_clip_stream_graph_and_workspace(ff):
     graph.replay()
     torch.cuda.synchronize()
     assert float(norm) == float(norm3) and all(torch.equal(a, b) for a, b in zip(outs, outs2))
+
+
+# ------------------------------------------------------------------ refusals of tensor calls
+
+def test_integers_beyond_an_int_are_refused(ff):
+    """A group or act that a C int does not hold is refused, not cut to its low 32 bits (a
+    group so cut reads scales that its tensor does not have); nothing of the call runs."""
+    from roofline_gb300 import gemm
+    g = torch.Generator().manual_seed(2)
+    X = _mat(g, 2, 256, BF16)
+    q = torch.zeros((8, 128), dtype=torch.uint8, device="cuda")
+    s = torch.ones((8, 1), dtype=BF16, device="cuda")  # one group, as 2^32 + 32 would have
+    for group in (2 ** 32 + 32, 2 ** 32 + 128, 2 ** 63 - 1, 2 ** 63, -32, 0, 1.5, None):
+        with pytest.raises(ValueError):
+            ff.q4_matmul(X, q, s, group=group)
+        with pytest.raises(ValueError):
+            ff.q4_gated(X, q, s, q, s, group=group)
+    with pytest.raises(gemm.GemmError):  # an int, but not a group that there is
+        ff.q4_matmul(X, q, s, group=512)
+    X, Wg, Wu, dH = _case(3, 4, 8, 6, F32, "io")
+    _, G, U = ff.gated_ff(X, Wg, Wu, save=True)
+    for act in (2 ** 32, -2 ** 32, 2 ** 64, 1.5):
+        with pytest.raises(ValueError):
+            ff.gated_ff(X, Wg, Wu, act=act)
+        with pytest.raises(ValueError):
+            ff.gated_ff_backward(dH, X, Wg, Wu, G, U, act=act)
+    with pytest.raises(gemm.GemmError):
+        ff.gated_ff(X, Wg, Wu, act=4)
+    with pytest.raises(ValueError):
+        ff.clip_grad_norm([X], "much")
