@@ -63,13 +63,22 @@ int64_t integer(PyObject *o, const char *name, int64_t lo, int64_t hi) {
 int act_of(PyObject *o) { return (int)integer(o, "act", INT_MIN, INT_MAX); }
 int64_t group_of(PyObject *o) { return integer(o, "group", 1, INT_MAX); }
 
-// Leading dimension of a row-major matrix.  The row stride of a one-row
-// matrix is never used.
+// Leading dimension of the matrix that dimension `row` of a tensor counts the
+// rows of.  The stride of a single row is never used; a stride of 0 between
+// rows (an expanded tensor) is none that the library can be told: 0.
+int64_t leading(const Tensor &t, int row) {
+  const int64_t rows = t.size(row), cols = t.size(1 - row);
+  if (rows > 1 && cols > 0) return t.stride(row);
+  return cols > 0 ? cols : 1;
+}
+bool unit(const Tensor &t, int dim) { return t.size(dim) <= 1 || t.stride(dim) == 1; }
+
+// The same of a row-major matrix, with the checks.
 int64_t leading(const Tensor &t, const char *name) {
-  const int64_t rows = t.size(0), cols = t.size(1);
-  if (cols > 1 && t.stride(1) != 1) refuse(std::string(name) + " must have unit column stride");
-  const int64_t ld = rows > 1 ? t.stride(0) : cols;
-  return ld > 0 ? ld : 1;
+  if (!unit(t, 1)) refuse(std::string(name) + " must have unit column stride");
+  const int64_t ld = leading(t, 0);
+  if (ld < 1) refuse(std::string(name) + " must not be expanded along its rows");
+  return ld;
 }
 
 // The matrix that sets a call's type and device.
@@ -97,10 +106,10 @@ struct First {
 struct Weight {
   int64_t ld[2] = {0, 0};
   Weight(const Tensor &t, const char *name) {
-    const int64_t D = t.size(0), F = t.size(1);
-    if (t.stride(1) == 1 || F <= 1) ld[GEMM_OP_N] = std::max<int64_t>(D > 1 ? t.stride(0) : F, 1);
-    if (t.stride(0) == 1 || D <= 1) ld[GEMM_OP_T] = std::max<int64_t>(F > 1 ? t.stride(1) : D, 1);
-    if (!ld[0] && !ld[1]) refuse(std::string(name) + " must have a unit row or column stride");
+    if (unit(t, 1)) ld[GEMM_OP_N] = leading(t, 0);
+    if (unit(t, 0)) ld[GEMM_OP_T] = leading(t, 1);
+    if (!ld[0] && !ld[1])
+      refuse(std::string(name) + " must have a unit row or column stride, and not be expanded");
   }
 };
 

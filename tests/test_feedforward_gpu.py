@@ -566,3 +566,42 @@ def test_integers_beyond_an_int_are_refused(ff):
         ff.gated_ff(X, Wg, Wu, act=4)
     with pytest.raises(ValueError):
         ff.clip_grad_norm([X], "much")
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_expanded_matrices_are_refused(ff, dt):
+    """One value expanded to a column (or to a row of a W.t()) has one element behind it,
+    not one a row: refused, as input and as output.  One row expanded has no second row."""
+    M, D, F = 40, 24, 16
+    X, Wg, Wu, dH = _case(3, M, D, F, dt, "io")
+    one = torch.ones((1, 1), dtype=dt, device="cuda")
+    bad = []
+    wg1, wu1 = Wg[:1], Wu[:1]                               # D = 1
+    bad.append(lambda: ff.gated_ff(one.expand(M, 1), wg1, wu1))
+    bad.append(lambda: ff.gated_ff(X, one.expand(D, 1), Wu[:, :1]))   # F = 1
+    bad.append(lambda: ff.gated_ff(X, Wg[:, :1], one.expand(D, 1)))
+    bad.append(lambda: ff.gated_ff(X[:, :1], one.expand(1, F), wu1))  # D = 1, by columns
+    bad.append(lambda: ff.gated_ff(X, Wg[:, :1], Wu[:, :1], out=one.expand(M, 1)))
+    bad.append(lambda: ff.gated_ff(X[:1].expand(M, D), Wg, Wu))
+    _, G, U = ff.gated_ff(X, Wg[:, :1], Wu[:, :1], save=True)
+    f1 = torch.ones((1, 1), device="cuda").expand(M, 1)
+    d1 = dH[:, :1].contiguous()
+    for args in ((one.expand(M, 1), X, G, U), (d1, X, f1, U), (d1, X, G, f1)):
+        bad.append(lambda a=args: ff.gated_ff_backward(a[0], a[1], Wg[:, :1], Wu[:, :1], a[2], a[3]))
+    q = torch.zeros((1, 1), dtype=torch.uint8, device="cuda")
+    s = torch.ones((F, 1), dtype=dt, device="cuda")
+    bad.append(lambda: ff.q4_matmul(X[:, :2], q.expand(F, 1), s, group=32))
+    bad.append(lambda: ff.q4_matmul(one.expand(M, 1), torch.zeros((F, 1), dtype=torch.uint8,
+                                                                  device="cuda"), s, group=32))
+    bad.append(lambda: ff.q4_matmul(X[:, :2], torch.zeros((1, 1), dtype=torch.uint8, device="cuda"),
+                                    s[:1], group=32, out=one.expand(M, 1)))
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    # what is expanded along one row or column only, or empty, is what it says
+    row = torch.randn((1, D), generator=torch.Generator().manual_seed(4)).to(dt).cuda()
+    h = ff.gated_ff(row.expand(1, D), Wg, Wu)
+    torch.cuda.synchronize()
+    assert ref.worst(h, ref.forward(row, Wg, Wu, "silu")["H"]) <= 1.0
+    assert ff.gated_ff(one.expand(0, 1), wg1, wu1).shape == (0, F)
+    assert ff.gated_ff(one[:, :0].expand(M, 0), Wg[:0], Wu[:0]).shape == (M, F)
