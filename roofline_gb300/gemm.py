@@ -336,16 +336,24 @@ def _operand(t, name):
     import torch
     if not (t.is_cuda and t.dtype == torch.float32 and t.dim() == 2):
         raise ValueError(f"{name} must be a 2-D float32 CUDA tensor")
-    # A stride along a dimension of length 1 is never used (torch may report
-    # any value there), so the leading dimension is then at least the row
-    # length of the stored matrix.
     if t.stride(1) == 1 or t.shape[1] <= 1:
-        ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-        return OP_N, max(ld, 1)
+        return OP_N, _leading(t, 0, name)
     if t.stride(0) == 1 or t.shape[0] <= 1:
-        ld = t.stride(1) if t.shape[1] > 1 else max(t.stride(1), t.shape[0])
-        return OP_T, max(ld, 1)
+        return OP_T, _leading(t, 1, name)
     raise ValueError(f"{name} must have a unit row or column stride")
+
+
+def _leading(t, row, name):
+    """The leading dimension of the matrix whose rows dimension `row` counts.
+    A stride along a dimension of length 1 is never used (torch may report any
+    value there), so the leading dimension is then at least the row length of
+    the stored matrix.  A stride of 0 between rows (an expanded tensor) is
+    none that the library takes."""
+    rows, cols = t.shape[row], t.shape[1 - row]
+    ld = t.stride(row)
+    if rows > 1 and cols > 0 and ld < 1:
+        raise ValueError(f"{name} must not be expanded along its rows")
+    return max(ld if rows > 1 else max(ld, cols), 1)
 
 
 def matmul(A, B, C=None, alpha=1.0, beta=0.0, mode=MODE_AUTO, stream=None,
@@ -397,9 +405,7 @@ def _host_matrix(t, name):
     if not (t.device.type == "cpu" and t.dtype == torch.float32 and t.dim() == 2 and
             (t.stride(1) == 1 or t.shape[1] <= 1)):
         raise ValueError(f"{name} must be a 2-D float32 CPU tensor with unit column stride")
-    # the row stride of a one-row matrix is never used (torch may report any value)
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-    return max(ld, 1)
+    return _leading(t, 0, name)
 
 
 def matmul_host(A, B, C=None, alpha=1.0, beta=0.0, mode=MODE_AUTO, blocks=0):

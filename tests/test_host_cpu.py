@@ -52,3 +52,22 @@ def test_matmul_host_rejects_device_or_strided_tensors(lib):
         gemm.matmul_host(torch.zeros(4, 8, dtype=torch.float64), torch.zeros(8, 3))
     with pytest.raises(ValueError):
         gemm.matmul_host(A, torch.zeros(7, 3))       # inner dimensions differ
+
+
+def test_matmul_host_rejects_expanded_tensors(lib):
+    """One value expanded to a column has one element behind it, not one a row."""
+    import torch
+    one = torch.ones((1, 1))
+    with pytest.raises(ValueError):
+        gemm.matmul_host(one.expand(500, 1), torch.zeros(1, 3))
+    with pytest.raises(ValueError):
+        gemm.matmul_host(torch.zeros(4, 500), one.expand(500, 1))
+    with pytest.raises(ValueError):
+        gemm.matmul_host(torch.zeros(500, 2), torch.zeros(2, 1), one.expand(500, 1))
+    with pytest.raises(ValueError):
+        gemm._leading(torch.ones((1, 1)).expand(1, 500), 1, "B")   # by columns
+    # one row, no columns, or an ordinary column of a wider buffer
+    assert gemm._leading(one.expand(1, 1), 0, "A") == 1
+    assert gemm._leading(torch.zeros((7, 3))[:, :1], 0, "A") == 3
+    assert gemm._leading(torch.zeros((1, 3))[:, :2], 0, "A") == 3
+    assert gemm._leading(one[:, :0].expand(5, 0), 0, "A") >= 1
