@@ -453,7 +453,7 @@ ff_tc_kernel(const __grid_constant__ FfLaunch l) {
   if (warp == 0) {
     // ---------------- producer: this CTA's rows of A and columns of B
     if (lane == 0 && !l.stall_producer) {
-      uint32_t s = 0, ph = 1, issued = 0;
+      uint32_t s = 0, ph = 1;
       auto take = [&] {
         ok = ff_wait(&empty[s], ph, l.wait_ns, abort_flag);
         return ok;
@@ -472,7 +472,7 @@ ff_tc_kernel(const __grid_constant__ FfLaunch l) {
         const TileAt at = tile_at(p, t);
         const int32_t m0 = (int32_t)(at.m * (CG * 128) + rank * 128);
         const int32_t n0 = (int32_t)(at.n * p.out_cols);
-        for (int kb = 0; kb < kbs && take(); ++kb, ++issued, next()) {
+        for (int kb = 0; kb < kbs && take(); ++kb, next()) {
           if (rank == 0) mbar_expect_tx(&full[s], CG * P * (uint32_t)(p.a_bytes + p.b_bytes));
           const uint32_t bar =
               CG == 1 ? smem_u32(&full[s]) : map_to_cta(smem_u32(&full[s]), 0);
@@ -510,8 +510,10 @@ ff_tc_kernel(const __grid_constant__ FfLaunch l) {
           load(std::integral_constant<int, 1>(), t);
       }
       // Every stage handed back: no load is in flight and no arrival from the
-      // pair's MMAs still on its way here.
-      for (uint32_t i = 0; i < stages && i < issued && ok; ++i) {
+      // pair's MMAs still on its way here.  All stages in turn, from the next one
+      // on: of one that was never filled the wait passes at once, and the last one
+      // filled is the last one waited for.
+      for (uint32_t i = 0; i < stages && ok; ++i) {
         take();
         next();
       }

@@ -81,6 +81,25 @@ def test_products_that_fill_the_gpu(ff, size, dt, order):
     _check_backward(ff, dH, X, Wg, Wu, G, U, "silu")
 
 
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [(2300, 64, 2200), (2300, 200, 2200), (2200, 2300, 130),
+                                  (2048, 256, 2304)])
+def test_fewer_blocks_of_k_than_stages(ff, size, dt):
+    """Sums so short that a worker's blocks of K do not fill the ring of stages (tiles of
+    pairs, and of one CTA): call after call, where each finds the shared memory and the
+    tensor memory as the one before it left them, gives the same bits."""
+    from roofline_gb300 import gemm
+    X, Wg, Wu, dH = _case(sum(size), *size, dt, "oi")
+    G, U = _check_forward(ff, X, Wg, Wu, "silu")
+    H = ff.gated_ff(X, Wg, Wu)
+    grads = ff.gated_ff_backward(dH, X, Wg, Wu, G, U)
+    for _ in range(20):
+        assert torch.equal(ff.gated_ff(X, Wg, Wu), H)
+        for a, b in zip(ff.gated_ff_backward(dH, X, Wg, Wu, G, U), grads):
+            assert torch.equal(a, b)
+    assert gemm.check_status() == gemm.OK
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_activations(ff, dt, act):
