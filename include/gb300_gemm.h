@@ -532,8 +532,13 @@ GEMM_API int gated_ff_workspace(int backward, int dtype, int op_w, int64_t M, in
  * of byte i.  S, Z: N x ceil(K / group) scales and zero points, contiguous,
  * of the same dtype as X and Y; Z may be NULL (every zero point 8).
  * group: 32, 64, 128 or 256.  dtype F32 or BF16; products are summed in
- * FP32 and exact to FP32 in F32, where an Inf in X gives NaN.  The weights
- * are read once for every 16 tokens (BF16) or 4 (F32): meant for M up to a few
+ * FP32 and exact to FP32 in F32.  In BF16 a group's sum of (128 + q) x is
+ * taken first and (128 + z) sum x off it, which leaves about 19 of FP32's 24
+ * bits.  An Inf or NaN in X gives what IEEE rules make of the formula, and sums
+ * that pass FP32's range on the way are computed again in a wider one: a
+ * result that the type can hold comes out (tokens of such sums take many
+ * times as long: a millisecond where others take 60 us).  The weights are
+ * read once for every 16 tokens (BF16) or 4 (F32): meant for M up to a few
  * dozen, and M up to 262,140 is accepted (GEMM_ERR_UNSUPPORTED beyond).
  * ldq < 2^32.
  */

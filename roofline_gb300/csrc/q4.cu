@@ -161,7 +161,8 @@ struct Raw8 {
 // The pairs (x_i, x_i+4), i = 0..3, of plane `plane`.  FP32 is cut, not
 // rounded, into its planes, which cannot overflow and takes four operations a
 // value: the first two 8 bits of the fraction with their leading one, the last
-// what is left, 8 bits too.  An Inf leaves NaN in its second and third.
+// what is left, 8 bits too.  An Inf leaves NaN in its second and third, for
+// which formula_sums() answers.
 __device__ __forceinline__ void pairs(const Raw8<bf16> &r, int, uint32_t (&b)[4]) {
   const uint4 v = r.v[0];
   b[0] = __byte_perm(v.x, v.z, 0x5410);
@@ -211,6 +212,88 @@ struct Q4Cfg {
   static constexpr int SM_WARPS = BY_SMEM < BY_REGS ? BY_SMEM / 4 * 4 : BY_REGS;
   static constexpr int MAX_WARPS = SM_WARPS < kMaxWarps ? SM_WARPS : kMaxWarps;
 };
+
+// Eight values of x from k on, zeros from K on.
+template <typename T>
+__device__ __forceinline__ void load_x(const Q4Args &p, const T *x, int64_t k, float (&v)[8]) {
+  __align__(16) T t[8];
+  if (p.vec_x && k + 8 <= p.K) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      reinterpret_cast<uint4 *>(t)[i] = __ldg(reinterpret_cast<const uint4 *>(x + k) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = k + i < p.K ? x[k + i] : from_f32<T>(0.0f);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
+}
+
+// Whether token m has a NaN, by one warp.
+template <typename T>
+__device__ __noinline__ bool has_nan(const Q4Args &p, int64_t m) {
+  const T *x = static_cast<const T *>(p.x) + m * p.ldx;
+  bool nan = false;
+#pragma unroll 4
+  for (int64_t k = (threadIdx.x & 31) * 8; k < p.K; k += 256) {
+    float v[8];
+    load_x(p, x, k, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) nan = nan || v[i] != v[i];
+  }
+  return __any_sync(0xffffffffu, nan);
+}
+
+// sum_k x(m,k) W(n + i,k), i = 0..7, of one matrix again, by the formula, by one
+// warp: for the sums that the tiles' arithmetic leaves Inf or NaN.  Those
+// include an Inf of X (which leaves NaN there) and sums that are finite: in BF16
+// a group's 128 + q and in FP32 its q - 8 can pass FP32's range where s (q - z)
+// x does not.  Eight codes' products in FP32, scaled by 2^-16 where an x is
+// beyond 2^112, so that none of them and no sum of them overflows for any zero
+// point below 2^9; the scales and the sum in 64 bits, which hold every product.
+// Lane i gets row i's sum; rows that the matrix does not have stand for its last.
+// What costs here is latency: 16 tokens by 8192 x 28672 take 61 us, 1.1 ms where
+// one token has an Inf and 0.1 where it has a NaN, for which has_nan() answers.
+template <typename T>
+__device__ __noinline__ float formula_sums(const Q4Args &p, int side, int64_t m, int64_t n) {
+  constexpr int R = 8;
+  const int lane = threadIdx.x & 31;
+  const Q4Side &w = p.w[side];
+  const T *x = static_cast<const T *>(p.x) + m * p.ldx;
+  double sum[R];
+#pragma unroll
+  for (int j = 0; j < R; ++j) sum[j] = 0.0;
+  for (int64_t k = lane * 8; k < p.K; k += 256) {
+    float v[8], most = 0.0f;
+    load_x(p, x, k, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]));
+    const bool large = most >= 0x1p112f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = large ? v[i] * 0x1p-16f : v[i];
+    const int there = (int)(p.K - k < 8 ? p.K - k : 8);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t row = n + j < p.N ? n + j : p.N - 1, at = row * p.groups + (k >> p.group_shift);
+      const uint8_t *q = w.q + row * w.ldq + k / 2;
+      const float zero = w.z ? to_f32(static_cast<const T *>(w.z)[at]) : 8.0f;
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < there) part = fmaf((float)(q[i / 2] >> (i % 2 * 4) & 15) - zero, v[i], part);
+      sum[j] = fma((double)to_f32(static_cast<const T *>(w.s)[at]),
+                   (double)part * (large ? 0x1p16 : 1.0), sum[j]);
+    }
+  }
+  float mine = 0.0f;
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+    if (lane == j) mine = (float)sum[j];
+  }
+  return mine;
+}
 
 template <typename T, int W, int TI, int NT, bool GATED>
 __global__ void __launch_bounds__(Q4Cfg<T, W, TI, NT, GATED>::SM_WARPS * 32, 1)
@@ -538,15 +621,35 @@ q4_kernel(const Q4Args p) {
       }
     return v;
   };
-  const int tokens = (int)(p.M - m0 < TOKENS ? p.M - m0 : TOKENS);
-  for (int e = rank * blockDim.x + tid; e < ROWS * tokens; e += p.split * blockDim.x) {
-    const int r = e % ROWS, m = e / ROWS;
-    if (r >= left) continue;
-    float y = total(r, m);
-    if constexpr (GATED) {
-      const float u = total(ROWS + r, m);
-      with_act(p.act, [&](auto a) { y = act_of<decltype(a)::value>(y) * u; });
+  const int tokens = (int)(p.M - m0 < TOKENS ? p.M - m0 : TOKENS), all = ROWS * tokens;
+  // a warp's 32 outputs at a time: all its lanes take part in formula_sums(),
+  // which has eight rows of one token
+  for (int e0 = rank * (int)blockDim.x + tid - lane; e0 < all; e0 += p.split * (int)blockDim.x) {
+    const int e = e0 + lane, r = e % ROWS, m = e / ROWS;
+    const bool here = e < all && r < left;
+    float y = 0.0f, u = 0.0f;
+    if (here) {
+      y = total(r, m);
+      if constexpr (GATED) u = total(ROWS + r, m);
     }
+    const bool bad = !isfinite(y) || !isfinite(u);
+    const uint32_t again = __ballot_sync(0xffffffffu, bad);
+    for (int of = 0; again != 0 && of < 32; of += 8) {
+      if ((again >> of & 0xffu) == 0) continue;
+      const int64_t om = m0 + (e0 + of) / ROWS, on = n0 + (e0 + of) % ROWS;
+      float v[2] = {__int_as_float(0x7fc00000), __int_as_float(0x7fc00000)};
+      if (!has_nan<T>(p, om)) {
+#pragma unroll
+        for (int k = 0; k < (GATED ? 2 : 1); ++k) v[k] = formula_sums<T>(p, k, om, on);
+      }
+#pragma unroll
+      for (int k = 0; k < (GATED ? 2 : 1); ++k)
+        v[k] = __shfl_sync(0xffffffffu, v[k], lane & 7);
+      if (bad && lane >= of && lane < of + 8) y = v[0], u = GATED ? v[1] : 0.0f;
+    }
+    if (!here) continue;
+    if constexpr (GATED)
+      with_act(p.act, [&](auto a) { y = act_of<decltype(a)::value>(y) * u; });
     static_cast<T *>(p.y)[(m0 + m) * p.ldy + n0 + r] = from_f32<T>(y);
   }
   if (p.split > 1) cluster_sync();  // the others have read this CTA's sums

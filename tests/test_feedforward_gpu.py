@@ -403,6 +403,75 @@ def test_q4_empty_and_nan(ff, dt):
     assert bool(Y[4].isnan().all())
 
 
+def _by_ieee(got, want, bound):
+    """NaN where the formula's value is NaN, Inf of its sign where it is Inf or beyond the
+    type, and within the bound elsewhere."""
+    got = got.cpu()
+    assert torch.equal(got.isnan(), want.isnan())
+    ok = ~want.isnan()
+    assert ref.worst(got[ok], (want[ok], bound[ok])) <= 1.0
+
+
+# few and many rows, sums that several thread blocks share, one token to three passes
+Q4_RANGE_SIZES = [(1, 40, 256), (2, 200, 300), (5, 33, 8200), (19, 70, 999), (40, 24, 513)]
+
+
+@pytest.mark.parametrize("group", [32, 128, 256])
+@pytest.mark.parametrize("zeros", [False, True], ids=["z8", "zeros"])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", Q4_RANGE_SIZES)
+def test_q4_inf_by_ieee_rules(ff, size, dt, zeros, group):
+    """Inf and NaN in X end where the formula in 64 bits says: Inf of the sign of the weight
+    that one Inf meets, NaN where it meets a weight of zero, an Inf of the other sign or a
+    NaN; tokens without any are as they were."""
+    M, N, K = size
+    g = torch.Generator().manual_seed(sum(size) + group)
+    X = _mat(g, M, K, dt).clone()
+    w, u = _quant(g, N, K, group, dt, zeros), _quant(g, N, K, group, dt, zeros)
+    if zeros:
+        for t in (w[2], u[2]):
+            t[::3] = 5.0  # zero points that codes meet
+    X[0, K // 3] = math.inf
+    if M > 1:
+        X[M - 1, K - 1] = -math.inf
+    if M > 4:
+        X[2, 1], X[2, K - 2] = math.inf, -math.inf
+        X[3, 4] = math.nan
+    Y = ff.q4_matmul(X, w[0], w[1], zeros=w[2], group=group)
+    H = ff.q4_gated(X, w[0], w[1], u[0], u[1], zeros_g=w[2], zeros_u=u[2], group=group, act="relu")
+    again = ff.q4_matmul(X, w[0], w[1], zeros=w[2], group=group)
+    torch.cuda.synchronize()
+    clean = X.clone()
+    clean[~X.isfinite()] = 0
+    bound, bound_h = ref.q4_rounded(clean, *w, group)[1], ref.q4_gated(clean, w, u, group, "relu")[1]
+    want, want_u = ref.q4(X, *w, group)[0], ref.q4(X, *u, group)[0]
+    assert not bool(want[0].isfinite().any()) and bool(want[0].isinf().any())
+    _by_ieee(Y, want, bound)
+    _by_ieee(H, torch.clamp(want, min=0) * want_u, bound_h)
+    assert torch.equal(Y.nan_to_num(), again.nan_to_num())
+
+
+@pytest.mark.parametrize("group", [32, 128, 256])
+@pytest.mark.parametrize("zeros", [False, True], ids=["z8", "zeros"])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", Q4_RANGE_SIZES)
+def test_q4_large_values(ff, size, dt, zeros, group):
+    """X near the end of the type's range, of one sign in some tokens, by scales that bring
+    the exact sums back into it: what is representable comes out, within the bounds."""
+    M, N, K = size
+    g = torch.Generator().manual_seed(sum(size) + group + 1)
+    X = torch.randn((M, K), generator=g).clamp(-4, 4)
+    X[::2] = X[::2].abs()
+    X = (X * 2.0 ** 125).to(dt).cuda()   # up to 2^127
+    q, s, z = _quant(g, N, K, group, dt, zeros)
+    s = (s.float() * 2.0 ** -16).to(dt)  # sums of K terms of about 2^(125 - 16 + 3) K^-1/2
+    Y = ff.q4_matmul(X, q, s, zeros=z, group=group)
+    torch.cuda.synchronize()
+    want = ref.q4_rounded(X, q, s, z, group)
+    assert float(want[0].abs().max()) < 3e38
+    assert ref.worst(Y, want) <= 1.0
+
+
 def test_q4_on_another_stream_and_in_a_graph(ff):
     g = torch.Generator().manual_seed(1)
     X = _mat(g, 1, 512, BF16)
