@@ -132,12 +132,41 @@ void call(const char *what, F f) {
   Py_END_ALLOW_THREADS if (rc != GEMM_OK) throw Failed{rc, what};
 }
 
-// The stream's handle: the one given, or (-1) torch's current one.
-cudaStream_t stream_of(PyObject *o, int device) {
-  const long long v = PyLong_AsLongLong(o);
-  if (v == -1) return c10::cuda::getCurrentCUDAStream(device).stream();
-  return reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(v));
-}
+// The stream of a call: the one whose handle is given, or (None) torch's current
+// one.  It is torch's current stream while this lives, so that new tensors are
+// of its memory: whatever used that before is ahead of the call in the stream.
+// (Of the caller's stream's memory, a kernel that is still to run there could
+// use it at the same time.)
+class OnStream {
+  c10::cuda::CUDAStream before_, on_;
+  c10::cuda::CUDAStreamGuard guard_;
+
+  static c10::cuda::CUDAStream of(PyObject *o, const c10::cuda::CUDAStream &current, int device) {
+    if (o == Py_None) return current;
+    const unsigned long long v = PyLong_AsUnsignedLongLong(o);
+    if (v == (unsigned long long)-1 && PyErr_Occurred()) {
+      PyErr_Clear();
+      refuse("stream: a stream's handle wanted");
+    }
+    return c10::cuda::getStreamFromExternal(
+        reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(v)), (c10::DeviceIndex)device);
+  }
+
+ public:
+  OnStream(PyObject *o, int device)
+      : before_(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device)),
+        on_(of(o, before_, device)), guard_(on_) {}
+  operator cudaStream_t() const { return on_.stream(); }
+  // For the caching allocator, when they are freed: a new tensor is used on the
+  // caller's stream too, one that the caller gave on this one.
+  void made(const Tensor &t) const { note(t, before_); }
+  void given(const Tensor &t) const { note(t, on_); }
+
+ private:
+  void note(const Tensor &t, const c10::cuda::CUDAStream &s) const {
+    if (t.defined() && on_.stream() != before_.stream()) t.record_stream(s.unwrap());
+  }
+};
 void *pointer_of(PyObject *o) {
   return o == Py_None ? nullptr : reinterpret_cast<void *>(PyLong_AsUnsignedLongLong(o));
 }
@@ -166,23 +195,26 @@ PyObject *gated_ff_(PyObject *const *a) {
   check(wu, "Wu", D, F, x.type, x.device);
   const Weight g(wg, "Wg"), u(wu, "Wu");
   const int op = common_op(g, u), act = act_of(a[3]);
-  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.device);
+  const OnStream s(a[6], x.device);
   Tensor H, G, U;
   int64_t ldh = positive(F);
   if (a[5] == Py_None) {
     H = x.make({M, F}, {F, 1}, x.type);
+    s.made(H);
   } else {
     H = tensor(a[5], "out");
     check(H, "out", M, F, x.type, x.device);
     ldh = leading(H, "out");
+    s.given(H);
   }
   const int64_t lds = (positive(F) + 7) / 8 * 8;  // rows on 16-byte boundaries, for wide stores
   const bool save = a[4] == Py_True;
   if (save) {
     G = x.make({M, F}, {lds, 1}, at::kFloat);
     U = x.make({M, F}, {lds, 1}, at::kFloat);
+    s.made(G);
+    s.made(U);
   }
-  const cudaStream_t s = stream_of(a[6], x.device);
   void *ws = pointer_of(a[7]);
   const size_t bytes = PyLong_AsSize_t(a[8]);
   call("gated_ff", [&] {
@@ -207,7 +239,7 @@ PyObject *gated_ff_backward_(PyObject *const *a) {
   const Weight g(wg, "Wg"), u(wu, "Wu");
   const int op = common_op(g, u), act = act_of(a[6]);
   const int64_t ldh = leading(dh, "dH"), ldg = leading(G, "G"), ldu = leading(U, "U");
-  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.device);
+  const OnStream s(a[9], x.device);
   Tensor dX, dWg, dWu;
   if (a[7] == Py_True) dX = x.make({M, D}, {D, 1}, x.type);
   if (a[8] == Py_True) {
@@ -215,8 +247,8 @@ PyObject *gated_ff_backward_(PyObject *const *a) {
     dWg = x.make({D, F}, {s0, s1}, x.type);
     dWu = x.make({D, F}, {s0, s1}, x.type);
   }
+  for (const Tensor *t : {&dX, &dWg, &dWu}) s.made(*t);
   const int64_t ldw = positive(op == GEMM_OP_N ? F : D);
-  const cudaStream_t s = stream_of(a[9], x.device);
   void *ws = pointer_of(a[10]);
   const size_t bytes = PyLong_AsSize_t(a[11]);
   if (dX.defined() || dWg.defined())
@@ -265,17 +297,18 @@ PyObject *q4_matmul_(PyObject *const *a) {
   const First x(a[0], "X");
   const int64_t group = group_of(a[4]), N = rows_of(a[1], "Wq");
   const Quantised w(a[1], a[2], a[3], N, x, group, "Wq");
-  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.device);
+  const OnStream s(a[6], x.device);
   Tensor Y;
   int64_t ldy = positive(N);
   if (a[5] == Py_None) {
     Y = x.make({x.rows, N}, {N, 1}, x.type);
+    s.made(Y);
   } else {
     Y = tensor(a[5], "out");
     check(Y, "out", x.rows, N, x.type, x.device);
     ldy = leading(Y, "out");
+    s.given(Y);
   }
-  const cudaStream_t s = stream_of(a[6], x.device);
   call("q4_matmul", [&] {
     return q4_matmul(x.dtype, x.rows, N, x.cols, x.t.data_ptr(), x.ld, w.q.data_ptr(), w.ldq,
                      w.s.data_ptr(), w.z, (int)group, Y.data_ptr(), ldy, s);
@@ -289,17 +322,18 @@ PyObject *q4_gated_(PyObject *const *a) {
   const int64_t group = group_of(a[7]), N = rows_of(a[1], "Wq_g");
   const Quantised g(a[1], a[2], a[3], N, x, group, "Wq_g"), u(a[4], a[5], a[6], N, x, group, "Wq_u");
   const int act = act_of(a[8]);
-  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)x.device);
+  const OnStream s(a[10], x.device);
   Tensor H;
   int64_t ldh = positive(N);
   if (a[9] == Py_None) {
     H = x.make({x.rows, N}, {N, 1}, x.type);
+    s.made(H);
   } else {
     H = tensor(a[9], "out");
     check(H, "out", x.rows, N, x.type, x.device);
     ldh = leading(H, "out");
+    s.given(H);
   }
-  const cudaStream_t s = stream_of(a[10], x.device);
   call("q4_gated", [&] {
     return q4_gated(x.dtype, act, x.rows, N, x.cols, x.t.data_ptr(), x.ld, g.q.data_ptr(), g.ldq,
                     g.s.data_ptr(), g.z, u.q.data_ptr(), u.ldq, u.s.data_ptr(), u.z, (int)group,
@@ -340,9 +374,9 @@ PyObject *grad_norm_clip_(PyObject *const *a) {
     refuse("max_norm must be a number");
   }
   if (device < 0) device = c10::cuda::current_device();
-  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
+  const OnStream s(a[3], device);
   Tensor norm = at::empty({}, at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, device));
-  const cudaStream_t s = stream_of(a[3], device);
+  s.made(norm);
   void *ws = pointer_of(a[4]);
   const size_t bytes = PyLong_AsSize_t(a[5]);
   call("grad_norm_clip", [&] {

@@ -7,6 +7,11 @@ rules of each call).  Tensors are torch CUDA tensors, float32 or bfloat16.
 The checks of the tensors are native (csrc/torch_binding.cpp); a tensor of
 the wrong shape, type, device or storage raises ValueError, what the library
 refuses raises ``gemm.GemmError``.
+
+``stream``: the torch.cuda.Stream to launch on (None: torch's current one).  As
+with torch's own operators its order with the streams that made the inputs, or
+that use the outputs, is the caller's part; new outputs are of the given
+stream's memory, so nothing before the call uses them.
 """
 from __future__ import annotations
 
@@ -57,17 +62,8 @@ def _workspace(w):
 
 
 def _handle(stream):
-    """The handle to launch on; -1 for torch's current stream."""
-    return -1 if stream is None else stream.cuda_stream
-
-
-def _made(stream, *new):
-    """New tensors come from torch's current stream; one that is used on
-    another is told so, for the caching allocator."""
-    if stream is not None:
-        for t in new:
-            if t is not None:
-                t.record_stream(stream)
+    """The handle of the stream to launch on; None for torch's current one."""
+    return None if stream is None else stream.cuda_stream
 
 
 def gated_ff(X, Wg, Wu, act="silu", save=False, out=None, stream=None, workspace=None):
@@ -77,10 +73,8 @@ def gated_ff(X, Wg, Wu, act="silu", save=False, out=None, stream=None, workspace
     ``gated_ff_backward`` reads.  ``workspace``: as for ``gemm.matmul``
     (``gated_ff_workspace`` bytes)."""
     ws, size = _workspace(workspace)
-    r = (_module or _native()).gated_ff(X, Wg, Wu, _act(act), bool(save), out, _handle(stream), ws,
-                                        size)
-    _made(stream, *(r if save else (r,)))
-    return r
+    return (_module or _native()).gated_ff(X, Wg, Wu, _act(act), bool(save), out, _handle(stream),
+                                           ws, size)
 
 
 def gated_ff_backward(dH, X, Wg, Wu, G, U, act="silu", need_dx=True, need_dw=True, stream=None,
@@ -90,10 +84,8 @@ def gated_ff_backward(dH, X, Wg, Wu, G, U, act="silu", need_dx=True, need_dw=Tru
     ``W.t()``, dWg.t() is the contiguous F x D gradient of W).  What is not
     needed is None."""
     ws, size = _workspace(workspace)
-    r = (_module or _native()).gated_ff_backward(dH, X, Wg, Wu, G, U, _act(act), bool(need_dx),
-                                                 bool(need_dw), _handle(stream), ws, size)
-    _made(stream, *r)
-    return r
+    return (_module or _native()).gated_ff_backward(dH, X, Wg, Wu, G, U, _act(act), bool(need_dx),
+                                                    bool(need_dw), _handle(stream), ws, size)
 
 
 def gated_ff_workspace(M, D, F, dtype, op_w=OP_N, backward=False, aligned=False) -> int:
@@ -110,26 +102,20 @@ def q4_matmul(X, Wq, scales, zeros=None, group=128, out=None, stream=None):
     """Y = X @ W.t() with W (N x K) in 4-bit codes: Wq uint8 N x ceil(K/2), the
     even column's code in the low half of each byte; W(n,k) =
     scales(n, k // group) * (code - zeros(n, k // group)), zeros 8 when None."""
-    Y = (_module or _native()).q4_matmul(X, Wq, scales, zeros, group, out, _handle(stream))
-    _made(stream, Y)
-    return Y
+    return (_module or _native()).q4_matmul(X, Wq, scales, zeros, group, out, _handle(stream))
 
 
 def q4_gated(X, Wq_g, scales_g, Wq_u, scales_u, zeros_g=None, zeros_u=None, group=128,
              act="silu", out=None, stream=None):
     """H = act(X @ Wg.t()) * (X @ Wu.t()), both weights in the format of ``q4_matmul``."""
-    H = (_module or _native()).q4_gated(X, Wq_g, scales_g, zeros_g, Wq_u, scales_u, zeros_u, group,
-                                        _act(act), out, _handle(stream))
-    _made(stream, H)
-    return H
+    return (_module or _native()).q4_gated(X, Wq_g, scales_g, zeros_g, Wq_u, scales_u, zeros_u,
+                                           group, _act(act), out, _handle(stream))
 
 
 def grad_norm(grads, stream=None, workspace=None):
     """sqrt of the sum of squares over all tensors, as a 0-d float32 tensor."""
     ws, size = _workspace(workspace)
-    norm = (_module or _native()).grad_norm_clip(list(grads), None, 0.0, _handle(stream), ws, size)
-    _made(stream, norm)
-    return norm
+    return (_module or _native()).grad_norm_clip(list(grads), None, 0.0, _handle(stream), ws, size)
 
 
 def clip_grad_norm(grads, max_norm, out=None, stream=None, workspace=None):
@@ -137,7 +123,5 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None, workspace=None):
     norm before clipping.  In place, or into the tensors ``out``."""
     grads = list(grads)
     ws, size = _workspace(workspace)
-    norm = (_module or _native()).grad_norm_clip(grads, grads if out is None else list(out),
+    return (_module or _native()).grad_norm_clip(grads, grads if out is None else list(out),
                                                  max_norm, _handle(stream), ws, size)
-    _made(stream, norm)
-    return norm

@@ -693,3 +693,66 @@ def test_expanded_matrices_are_refused(ff, dt):
     assert ref.worst(h, ref.forward(row, Wg, Wu, "silu")["H"]) <= 1.0
     assert ff.gated_ff(one.expand(0, 1), wg1, wu1).shape == (0, F)
     assert ff.gated_ff(one[:, :0].expand(M, 0), Wg[:0], Wu[:0]).shape == (M, F)
+
+
+# ------------------------------------------------------------------ streams and memory
+
+def _calls(ff):
+    """{name: f(stream) -> its new tensors} of every operator, on inputs that stay."""
+    g = torch.Generator().manual_seed(5)
+    M, D, F = 70, 96, 264
+    X, Wg, Wu, dH = _case(5, M, D, F, BF16, "oi")
+    _, G, U = ff.gated_ff(X, Wg, Wu, save=True)
+    w = _quant(g, F, D, 32, BF16, True)
+    grads = [X, dH, G]
+    outs = [torch.empty_like(t) for t in grads]
+    return {
+        "forward": lambda s: ff.gated_ff(X, Wg, Wu, save=True, stream=s),
+        "backward": lambda s: ff.gated_ff_backward(dH, X, Wg, Wu, G, U, stream=s),
+        "q4": lambda s: (ff.q4_matmul(X, w[0], w[1], zeros=w[2], group=32, stream=s),),
+        "q4 gated": lambda s: (ff.q4_gated(X, w[0], w[1], w[0], w[1], zeros_g=w[2], zeros_u=w[2],
+                                           group=32, stream=s),),
+        "norm": lambda s: (ff.grad_norm(grads, stream=s),),
+        "clip": lambda s: (ff.clip_grad_norm(grads, 0.5, out=outs, stream=s),),
+    }
+
+
+def _write_later(tensors):
+    """Frees blocks of these tensors' sizes on the current stream, with writes to them
+    enqueued there that run some 25 ms from now."""
+    blocks = [torch.empty(t.untyped_storage().nbytes(), dtype=torch.uint8, device="cuda")
+              for t in tensors]
+    torch.cuda._sleep(50_000_000)
+    for b in blocks:
+        b.fill_(7)
+
+
+@pytest.mark.parametrize("name", ["forward", "backward", "q4", "q4 gated", "norm", "clip"])
+def test_new_outputs_on_another_stream(ff, name):
+    """Memory that the current stream is still to write is not given to a call on another
+    stream that does not wait for it; what the current stream enqueues on an output after
+    waiting for the call is done before the output's memory is used again there."""
+    call = _calls(ff)[name]
+    want = call(None)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        _write_later(want)
+        got = call(side)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    # used on the current stream behind 25 ms of work, freed, and allocated again on `side`
+    copies = [torch.empty_like(t) for t in got]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    for c, t in zip(copies, got):
+        c.copy_(t)
+    del got, t, a, b
+    more = call(side)
+    with torch.cuda.stream(side):
+        for m in more:
+            m.fill_(7)
+    torch.cuda.synchronize()
+    for c, b in zip(copies, want):
+        assert torch.equal(c, b)
