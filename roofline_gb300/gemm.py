@@ -356,6 +356,21 @@ def _leading(t, row, name):
     return max(ld if rows > 1 else max(ld, cols), 1)
 
 
+def _new_output(M, N, device, stream):
+    """A float32 matrix of the memory of the stream that writes it (None:
+    torch's current one), so that whatever used that memory before is ahead of
+    the call; freed, it waits for the caller's stream too."""
+    import torch
+    if stream is None or device.type != "cuda":
+        return torch.empty((M, N), dtype=torch.float32, device=device)
+    before = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        C = torch.empty((M, N), dtype=torch.float32, device=device)
+    if before != stream:
+        C.record_stream(before)
+    return C
+
+
 def matmul(A, B, C=None, alpha=1.0, beta=0.0, mode=MODE_AUTO, stream=None,
            workspace=None):
     """C <- alpha * A @ B + beta * C for float32 CUDA tensors.
@@ -376,7 +391,7 @@ def matmul(A, B, C=None, alpha=1.0, beta=0.0, mode=MODE_AUTO, stream=None,
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs C")
-        C = torch.empty((M, N), dtype=torch.float32, device=A.device)
+        C = _new_output(M, N, A.device, stream)
     op_a, lda = _operand(A, "A")
     op_b, ldb = _operand(B, "B")
     op_c, ldc = _operand(C, "C")

@@ -796,3 +796,34 @@ def test_tc_b_split_knob_refuses_unbuilt_forms(monkeypatch):
     monkeypatch.setenv("GEMM_TC_CONFIG", "128,256,16,5,2,0,1")
     p = gemm.plan(2048, 2048, 2048, mode="tf32x3")
     assert not (p["bn"] == 256 and p["b_split_in_kernel"] == 1)
+
+
+def test_new_output_on_another_stream():
+    """C made by a call on a given stream is of that stream's memory: writes that the current
+    stream is still to make to a block that it freed do not meet it."""
+    import torch
+    from roofline_gb300 import gemm
+    g = torch.Generator().manual_seed(3)
+    A, B = torch.randn((100, 70), generator=g).cuda(), torch.randn((70, 260), generator=g).cuda()
+    want = gemm.matmul(A, B)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        block = torch.empty_like(want)
+        torch.cuda._sleep(50_000_000)  # some 25 ms
+        block.fill_(7)
+        del block
+        got = gemm.matmul(A, B, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    # read on the current stream behind 25 ms of work, freed, and its like made on `side`
+    copy = torch.empty_like(want)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    copy.copy_(got)
+    del got
+    more = gemm.matmul(A, B, stream=side)
+    with torch.cuda.stream(side):
+        more.fill_(7)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
