@@ -170,7 +170,9 @@ GEMM_API int gemm_f32(int64_t M, int64_t N, int64_t K, const float *A, int64_t l
  * when needed (which synchronises the device) and freed by gemm_shutdown();
  * that buffer is shared by every call on the device, so calls that use it
  * must not run at the same time on the GPU (issue them on one stream, or
- * give each concurrent stream its own workspace).
+ * give each concurrent stream its own workspace), and a graph captured with
+ * it must not be replayed after a call that grew it (give captured calls
+ * their own).
  * A call allocates nothing, synchronises nothing and reads nothing back to
  * the host when the workspace is given (or the library buffer is already
  * large enough), so it can be captured into a CUDA graph and replayed.
@@ -570,7 +572,7 @@ GEMM_API int q4_gated(int dtype, int act, int64_t M, int64_t N, int64_t K, const
  * outputs follow the formula).  The order of the sums is fixed: equal calls
  * give equal bits.
  * workspace: grad_norm_clip_workspace(count) bytes, 256-byte aligned, or
- * NULL for the library's per-device buffer.
+ * NULL for the library's per-device buffer (with the rules of gemm_f32_ex).
  */
 GEMM_API int grad_norm_clip(int64_t count, const int *dtypes, const void *const *grads,
                             void *const *outs, const int64_t *sizes, float max_norm,

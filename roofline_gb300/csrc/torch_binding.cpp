@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -167,8 +168,50 @@ class OnStream {
     if (t.defined() && on_.stream() != before_.stream()) t.record_stream(s.unwrap());
   }
 };
-void *pointer_of(PyObject *o) {
-  return o == Py_None ? nullptr : reinterpret_cast<void *>(PyLong_AsUnsignedLongLong(o));
+// A call's scratch: the caller's tensor, or torch's memory of the call's stream
+// while this lives.  (Not the library's one buffer per device: calls on two
+// streams would write it at once, and a graph would keep its address when a
+// larger call has freed it.)
+class Scratch {
+  void *own_ = nullptr;
+
+ public:
+  void *p = nullptr;
+  size_t bytes = 0;
+  Scratch(PyObject *given, uint64_t need, const OnStream &s, int device) {
+    if (given != Py_None) {
+      const Tensor &t = tensor(given, "workspace");
+      if (!t.is_cuda() || t.get_device() != device || !t.is_contiguous())
+        refuse("workspace must be a contiguous tensor on CUDA device " + std::to_string(device));
+      p = t.data_ptr();
+      bytes = t.nbytes();
+      s.given(t);
+    }
+    if (bytes == 0 && need > 0) {
+      p = own_ = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(need, s);
+      bytes = need;
+    }
+  }
+  Scratch(const Scratch &) = delete;
+  ~Scratch() {
+    if (own_) c10::cuda::CUDACachingAllocator::raw_delete(own_);
+  }
+};
+
+// Scratch bytes of the block: where BF16 matrices (data, leading dimension,
+// rows) all lie on 16-byte boundaries, those of aligned ones.
+struct Rows {
+  const void *p;
+  int64_t ld, rows;
+};
+uint64_t block_bytes(int backward, int dtype, int op, int64_t M, int64_t D, int64_t F,
+                     std::initializer_list<Rows> read) {
+  uint64_t need = 0;
+  bool aligned = true;
+  for (const Rows &r : read)
+    aligned = aligned && reinterpret_cast<uintptr_t>(r.p) % 16 == 0 && (r.rows == 1 || r.ld % 8 == 0);
+  // sizes that it refuses the call itself refuses too
+  return gated_ff_workspace(backward, dtype, op, M, D, F, aligned, &need) == GEMM_OK ? need : 0;
 }
 void *address(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 PyObject *wrap(const Tensor &t) {
@@ -186,7 +229,7 @@ PyObject *triple(const Tensor &a, const Tensor &b, const Tensor &c) {
   return r;
 }
 
-// gated_ff(X, Wg, Wu, act, save, out, stream, workspace, its bytes)
+// gated_ff(X, Wg, Wu, act, save, out, stream, workspace)
 PyObject *gated_ff_(PyObject *const *a) {
   const First x(a[0], "X");
   const Tensor &wg = tensor(a[1], "Wg"), &wu = tensor(a[2], "Wu");
@@ -215,17 +258,21 @@ PyObject *gated_ff_(PyObject *const *a) {
     s.made(G);
     s.made(U);
   }
-  void *ws = pointer_of(a[7]);
-  const size_t bytes = PyLong_AsSize_t(a[8]);
+  const int64_t wr = op == GEMM_OP_N ? D : F;
+  const Scratch ws(a[7],
+                   block_bytes(0, x.dtype, op, M, D, F,
+                               {{x.t.data_ptr(), x.ld, M}, {wg.data_ptr(), g.ld[op], wr},
+                                {wu.data_ptr(), u.ld[op], wr}}),
+                   s, x.device);
   call("gated_ff", [&] {
     return gated_ff(x.dtype, act, op, M, D, F, x.t.data_ptr(), x.ld, wg.data_ptr(), g.ld[op],
                     wu.data_ptr(), u.ld[op], H.data_ptr(), ldh, static_cast<float *>(address(G)),
-                    lds, static_cast<float *>(address(U)), lds, ws, bytes, s);
+                    lds, static_cast<float *>(address(U)), lds, ws.p, ws.bytes, s);
   });
   return save ? triple(H, G, U) : wrap(H);
 }
 
-// gated_ff_backward(dH, X, Wg, Wu, G, U, act, need_dx, need_dw, stream, workspace, its bytes)
+// gated_ff_backward(dH, X, Wg, Wu, G, U, act, need_dx, need_dw, stream, workspace)
 PyObject *gated_ff_backward_(PyObject *const *a) {
   const First x(a[1], "X");
   const Tensor &dh = tensor(a[0], "dH"), &wg = tensor(a[2], "Wg"), &wu = tensor(a[3], "Wu"),
@@ -249,16 +296,21 @@ PyObject *gated_ff_backward_(PyObject *const *a) {
   }
   for (const Tensor *t : {&dX, &dWg, &dWu}) s.made(*t);
   const int64_t ldw = positive(op == GEMM_OP_N ? F : D);
-  void *ws = pointer_of(a[10]);
-  const size_t bytes = PyLong_AsSize_t(a[11]);
-  if (dX.defined() || dWg.defined())
+  if (dX.defined() || dWg.defined()) {
+    const int64_t wr = op == GEMM_OP_N ? D : F;
+    const Scratch ws(a[10],
+                     block_bytes(1, x.dtype, op, M, D, F,
+                                 {{x.t.data_ptr(), x.ld, M}, {wg.data_ptr(), g.ld[op], wr},
+                                  {wu.data_ptr(), u.ld[op], wr}}),
+                     s, x.device);
     call("gated_ff_backward", [&] {
       return gated_ff_backward(
           x.dtype, act, op, M, D, F, dh.data_ptr(), ldh, x.t.data_ptr(), x.ld, wg.data_ptr(),
           g.ld[op], wu.data_ptr(), u.ld[op], static_cast<const float *>(G.data_ptr()), ldg,
           static_cast<const float *>(U.data_ptr()), ldu, address(dX), positive(D), address(dWg),
-          ldw, address(dWu), ldw, ws, bytes, s);
+          ldw, address(dWu), ldw, ws.p, ws.bytes, s);
     });
+  }
   return triple(dX, dWg, dWu);
 }
 
@@ -342,7 +394,7 @@ PyObject *q4_gated_(PyObject *const *a) {
   return wrap(H);
 }
 
-// grad_norm_clip(grads, outs, max_norm, stream, workspace, its bytes); lists, outs may be None
+// grad_norm_clip(grads, outs, max_norm, stream, workspace); lists, outs may be None
 PyObject *grad_norm_clip_(PyObject *const *a) {
   if (!PyList_Check(a[0]) || (a[1] != Py_None && !PyList_Check(a[1])))
     refuse("grads and out must be lists");
@@ -377,12 +429,11 @@ PyObject *grad_norm_clip_(PyObject *const *a) {
   const OnStream s(a[3], device);
   Tensor norm = at::empty({}, at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, device));
   s.made(norm);
-  void *ws = pointer_of(a[4]);
-  const size_t bytes = PyLong_AsSize_t(a[5]);
+  const Scratch ws(a[4], grad_norm_clip_workspace(n), s, device);
   call("grad_norm_clip", [&] {
     return grad_norm_clip(n, dtypes.data(), in.data(), a[1] == Py_None ? nullptr : out.data(),
-                          sizes.data(), (float)max_norm, static_cast<float *>(norm.data_ptr()), ws,
-                          bytes, s);
+                          sizes.data(), (float)max_norm, static_cast<float *>(norm.data_ptr()),
+                          ws.p, ws.bytes, s);
   });
   return wrap(norm);
 }
@@ -419,10 +470,10 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define FF_ENTRY(name, f, n) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(entry<f, n>)), METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {FF_ENTRY("gated_ff", gated_ff_, 9),
-                          FF_ENTRY("gated_ff_backward", gated_ff_backward_, 12),
+PyMethodDef kMethods[] = {FF_ENTRY("gated_ff", gated_ff_, 8),
+                          FF_ENTRY("gated_ff_backward", gated_ff_backward_, 11),
                           FF_ENTRY("q4_matmul", q4_matmul_, 7), FF_ENTRY("q4_gated", q4_gated_, 11),
-                          FF_ENTRY("grad_norm_clip", grad_norm_clip_, 6),
+                          FF_ENTRY("grad_norm_clip", grad_norm_clip_, 5),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ff_native", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -12,6 +12,12 @@ refuses raises ``gemm.GemmError``.
 with torch's own operators its order with the streams that made the inputs, or
 that use the outputs, is the caller's part; new outputs are of the given
 stream's memory, so nothing before the call uses them.
+
+``workspace``: optional contiguous CUDA tensor used as scratch
+(``gated_ff_workspace`` or ``grad_norm_workspace`` bytes, which no other work
+uses at the time).  Without one a call takes its own from torch's allocator, on
+the stream that it runs on: calls on several streams share nothing, and a
+captured graph keeps its own.
 """
 from __future__ import annotations
 
@@ -57,10 +63,6 @@ def _act(act) -> int:
     return code
 
 
-def _workspace(w):
-    return (None, 0) if w is None else (w.data_ptr(), w.numel() * w.element_size())
-
-
 def _handle(stream):
     """The handle of the stream to launch on; None for torch's current one."""
     return None if stream is None else stream.cuda_stream
@@ -70,11 +72,9 @@ def gated_ff(X, Wg, Wu, act="silu", save=False, out=None, stream=None, workspace
     """H = act(X @ Wg) * (X @ Wu): X is M x D, the weights D x F (a stored
     F x D weight is passed as ``W.t()``, without a copy).  Returns H, or with
     ``save`` (H, G, U), where G = X @ Wg and U = X @ Wu, in float32, are what
-    ``gated_ff_backward`` reads.  ``workspace``: as for ``gemm.matmul``
-    (``gated_ff_workspace`` bytes)."""
-    ws, size = _workspace(workspace)
+    ``gated_ff_backward`` reads."""
     return (_module or _native()).gated_ff(X, Wg, Wu, _act(act), bool(save), out, _handle(stream),
-                                           ws, size)
+                                           workspace)
 
 
 def gated_ff_backward(dH, X, Wg, Wu, G, U, act="silu", need_dx=True, need_dw=True, stream=None,
@@ -83,9 +83,8 @@ def gated_ff_backward(dH, X, Wg, Wu, G, U, act="silu", need_dx=True, need_dw=Tru
     weights' gradients are stored as the weights are (for a weight passed as
     ``W.t()``, dWg.t() is the contiguous F x D gradient of W).  What is not
     needed is None."""
-    ws, size = _workspace(workspace)
     return (_module or _native()).gated_ff_backward(dH, X, Wg, Wu, G, U, _act(act), bool(need_dx),
-                                                    bool(need_dw), _handle(stream), ws, size)
+                                                    bool(need_dw), _handle(stream), workspace)
 
 
 def gated_ff_workspace(M, D, F, dtype, op_w=OP_N, backward=False, aligned=False) -> int:
@@ -114,14 +113,18 @@ def q4_gated(X, Wq_g, scales_g, Wq_u, scales_u, zeros_g=None, zeros_u=None, grou
 
 def grad_norm(grads, stream=None, workspace=None):
     """sqrt of the sum of squares over all tensors, as a 0-d float32 tensor."""
-    ws, size = _workspace(workspace)
-    return (_module or _native()).grad_norm_clip(list(grads), None, 0.0, _handle(stream), ws, size)
+    return (_module or _native()).grad_norm_clip(list(grads), None, 0.0, _handle(stream),
+                                                 workspace)
+
+
+def grad_norm_workspace(count) -> int:
+    """Scratch bytes of ``grad_norm`` and ``clip_grad_norm`` of `count` tensors."""
+    return int(gemm.load().grad_norm_clip_workspace(count))
 
 
 def clip_grad_norm(grads, max_norm, out=None, stream=None, workspace=None):
     """Scales every tensor by min(1, max_norm / (norm + 1e-6)) and returns the
     norm before clipping.  In place, or into the tensors ``out``."""
     grads = list(grads)
-    ws, size = _workspace(workspace)
     return (_module or _native()).grad_norm_clip(grads, grads if out is None else list(out),
-                                                 max_norm, _handle(stream), ws, size)
+                                                 max_norm, _handle(stream), workspace)

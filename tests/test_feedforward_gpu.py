@@ -756,3 +756,82 @@ def test_new_outputs_on_another_stream(ff, name):
     torch.cuda.synchronize()
     for c, b in zip(copies, want):
         assert torch.equal(c, b)
+
+
+def test_calls_on_two_streams_at_once(ff):
+    """Calls without a workspace share none: on two streams at once, with other inputs, each
+    gives the bits that it gives alone."""
+    from roofline_gb300 import gemm
+    cases = [_case(20 + i, 300, 203, 1111, dt, "oi", 3) for i, dt in enumerate((F32, BF16))]
+    grads = [[torch.randn(50_000 + 999 * i + j).cuda() for j in range(20)] for i in range(2)]
+
+    def step(i, stream):
+        X, Wg, Wu, dH = cases[i]
+        H, G, U = ff.gated_ff(X, Wg, Wu, save=True, stream=stream)
+        return [H, G, U, *ff.gated_ff_backward(dH, X, Wg, Wu, G, U, stream=stream),
+                ff.grad_norm(grads[i], stream=stream)]
+    want = [step(i, None) for i in range(2)]
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for s in sides:
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)  # both queues fill before either runs
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            got[i].append(step(i, sides[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for call in got[i]:
+            for a, b in zip(call, want[i]):
+                assert torch.equal(a, b)
+    assert gemm.check_status() == gemm.OK
+
+
+def test_graph_keeps_its_workspace(ff):
+    """A captured call's scratch stays its own when a later call needs more."""
+    X, Wg, Wu, dH = _case(30, 100, 72, 136, F32, "io")
+    ts = [torch.randn(5000).cuda() for _ in range(10)]
+    H, G, U = ff.gated_ff(X, Wg, Wu, save=True)
+    want = [H, *ff.gated_ff_backward(dH, X, Wg, Wu, G, U), ff.grad_norm(ts)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        H2, G2, U2 = ff.gated_ff(X, Wg, Wu, save=True)
+        got = [H2, *ff.gated_ff_backward(dH, X, Wg, Wu, G2, U2), ff.grad_norm(ts)]
+    large = _case(31, 2000, 1024, 2816, F32, "io")
+    for _ in range(2):
+        _, G3, U3 = ff.gated_ff(*large[:3], save=True)
+        ff.gated_ff_backward(large[3], *large[:3], G3, U3)
+        ff.grad_norm([t for t in ts for _ in range(300)])
+        torch.cuda.synchronize()
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_workspaces_that_are_none_are_refused(ff):
+    from roofline_gb300 import gemm
+    X, Wg, Wu, dH = _case(6, 40, 64, 72, F32, "io")
+    _, G, U = ff.gated_ff(X, Wg, Wu, save=True)
+    need = ff.gated_ff_workspace(40, 64, 72, ff.DT_F32, backward=True)
+    host = torch.empty(need, dtype=torch.uint8)
+    one = torch.empty(1, dtype=torch.uint8, device="cuda").expand(need)
+    apart = torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]
+    for ws in (host, one, apart, 4096):
+        for call in (lambda: ff.gated_ff(X, Wg, Wu, workspace=ws),
+                     lambda: ff.gated_ff_backward(dH, X, Wg, Wu, G, U, workspace=ws),
+                     lambda: ff.grad_norm([X], workspace=ws),
+                     lambda: ff.clip_grad_norm([X], 1.0, workspace=ws)):
+            with pytest.raises(ValueError):
+                call()
+    ts = [X, G]
+    ws = torch.empty(ff.grad_norm_workspace(2), dtype=torch.uint8, device="cuda")
+    a, b = ff.grad_norm(ts, workspace=ws), ff.grad_norm(ts)
+    torch.cuda.synchronize()
+    assert float(a) == float(b)
+    with pytest.raises(gemm.GemmError):
+        ff.grad_norm(ts, workspace=ws[:8])
