@@ -371,9 +371,10 @@ GEMM_API const char *gemm_strerror(int code);
  * gemm_check_status -- the deferred half of that same CUDA_CHECK step
  * ("Starter scaffolding" checks cudaGetLastError and cudaDeviceSynchronize
  * after a launch): synchronises `stream`, then reads and clears the
- * library's device status words, set by the tensor-core kernel when one of
- * its bounded waits runs out and by the stream-K fix-up when a tile has more
- * parts than it can sum.  Returns GEMM_ERR_DEVICE_TIMEOUT or
+ * library's device status words on that stream, set by a tensor-core kernel
+ * (the GEMM's, the gated block's) when one of its bounded waits runs out and
+ * by the stream-K fix-up when a tile has more parts than it can sum.  A
+ * status of the block waits for the next call when the GEMM has one.  Returns GEMM_ERR_DEVICE_TIMEOUT or
  * GEMM_ERR_UNSUPPORTED if one was set (the result of the call that set it is
  * not valid), GEMM_ERR_CUDA if the synchronisation reported an error, else
  * GEMM_OK.  Blocking; not for use during stream capture.

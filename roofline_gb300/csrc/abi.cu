@@ -440,9 +440,9 @@ int gemm_check_status(cudaStream_t stream) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
-  const int ff = ff_read_and_clear_status();
+  // one status at a time: the block's stays for the next call when the GEMM has one
   const int tc = tc_read_and_clear_status(stream);
-  return tc != GEMM_OK ? tc : ff;
+  return tc != GEMM_OK ? tc : ff_read_and_clear_status(stream);
 }
 
 void gemm_shutdown(void) {

@@ -950,16 +950,19 @@ int launch_ff_products(const FfProduct *q, int n, const DeviceProps &dp, cudaStr
                                : launch_any<3, false>(q, n, dp, s);
 }
 
-// Called on a synchronised stream.
-int ff_read_and_clear_status() {
+int ff_read_and_clear_status(cudaStream_t s) {
   int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_ff_status, sizeof(int)) != cudaSuccess) {
+  if (cudaMemcpyFromSymbolAsync(&v, g_ff_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
   if (v != 0) {
     const int zero = 0;
-    if (cudaMemcpyToSymbol(g_ff_status, &zero, sizeof(int)) != cudaSuccess) {
+    if (cudaMemcpyToSymbolAsync(g_ff_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess) {
       cudaGetLastError();
       return GEMM_ERR_CUDA;
     }

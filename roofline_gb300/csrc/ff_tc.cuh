@@ -37,7 +37,7 @@ struct FfProduct {
 // Enqueues n products in one launch: one, or two that are not gated and of as
 // many planes, the one with longer sums first.  Returns a GEMM_* status.
 int launch_ff_products(const FfProduct *p, int n, const DeviceProps &dp, cudaStream_t s);
-int ff_read_and_clear_status();
+int ff_read_and_clear_status(cudaStream_t s);
 
 // Lays one matrix (rows x cols, row stride ld, FP32 or BF16) out as BF16
 // planes whose rows TMA can read: ld_out a multiple of 8, 16-byte aligned.

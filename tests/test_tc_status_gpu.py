@@ -73,3 +73,38 @@ def test_streaming_host_call_with_a_block_that_never_lands():
         del os.environ["GEMM_HOST_STREAM"]
     assert rc == gemm.OK, gemm.strerror(rc)
     assert oracle.mismatches(hC.numpy(), oracle.gemm(a, b)) == 0
+
+
+def test_status_waits_for_its_stream_only():
+    """gemm_check_status(stream) reads the status words on that stream: work on another one
+    (here the default stream, which every blocking stream would wait for) goes on."""
+    import torch
+    from roofline_gb300 import gemm
+    side = torch.cuda.Stream()
+    assert gemm.check_status() == gemm.OK
+    assert gemm.check_status(side.cuda_stream) == gemm.OK  # what a first use loads is loaded
+    torch.cuda.synchronize()
+    done = torch.cuda.Event()
+    torch.cuda._sleep(400_000_000)  # some 200 ms
+    done.record()
+    assert gemm.check_status(side.cuda_stream) == gemm.OK
+    assert not done.query()
+    torch.cuda.synchronize()
+
+
+def test_both_status_words_are_reported(monkeypatch):
+    """A stalled GEMM and a stalled block: each is reported once, one a call."""
+    import torch
+    from roofline_gb300 import feedforward as ff, gemm
+    A, B = torch.ones((256, 300), device="cuda"), torch.ones((300, 384), device="cuda")
+    X, W = (torch.ones(s, dtype=torch.bfloat16, device="cuda") for s in ((256, 64), (64, 128)))
+    assert gemm.check_status() == gemm.OK
+    with monkeypatch.context() as m:
+        m.setenv("GEMM_DEBUG_STALL_PRODUCER", "1")
+        m.setenv("GEMM_DEBUG_WAIT_LIMIT_NS", "2000000")  # 2 ms
+        gemm.matmul(A, B, mode="tf32x3")
+        ff.gated_ff(X, W, W)
+        torch.cuda.synchronize()
+    assert gemm.check_status() == gemm.ERR_DEVICE_TIMEOUT
+    assert gemm.check_status() == gemm.ERR_DEVICE_TIMEOUT
+    assert gemm.check_status() == gemm.OK
