@@ -4,7 +4,8 @@ of its feed-forward operators.
 Each .cu file in csrc/ is compiled to an object in parallel, then linked
 into one shared library (static CUDA runtime, no torch dependency).
 torch_binding.cpp becomes the Python module _ff_native.so beside it, built
-with g++ against the installed torch's headers.  Run
+with g++ against the installed torch's headers; without torch only the library
+is built.  Run
 ``python -m roofline_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -43,16 +44,19 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return _sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
+def _headers():
+    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(f) > t for f in _deps())
+def _stale(out: str, deps) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(f) > os.path.getmtime(out)
+                                          for f in deps)
+
+
+def _torch_dir():
+    """The installed torch's folder; None without torch, which only the binding needs."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
 
 
 def _compile(src: str, log_dir: str) -> str:
@@ -68,7 +72,7 @@ def _compile(src: str, log_dir: str) -> str:
 
 def _compile_binding(log_dir: str) -> str:
     """torch_binding.cpp to an object (its link needs the library)."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_dir = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     obj = os.path.join(BUILD, "torch_binding.o")
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
@@ -85,7 +89,7 @@ def _compile_binding(log_dir: str) -> str:
 
 
 def _link_binding(obj: str) -> None:
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_dir = _torch_dir()
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-shared", obj, "-o", tmp, "-L",
            os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
@@ -96,25 +100,33 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libgb300gemm.so and its torch binding if any source is
-    newer than they are."""
-    if not force and not _stale():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding, BUILD)
-        objs = list(ex.map(lambda s: _compile(s, BUILD), srcs))
-        binding_obj = binding.result()
+def _link(objs) -> None:
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC"] + objs + ["-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
-    if verbose:
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link what is older than its sources: libgb300gemm.so, then,
+    where torch is installed, its binding.  The library is there whatever
+    becomes of the binding, whose failure is raised last."""
+    srcs = _sources()
+    lib = force or _stale(LIB, srcs + _headers())
+    torch = _torch_dir() is not None and \
+        (lib or _stale(BINDING, [BINDING_SRC, LIB] + _headers()))
+    if not lib and not torch:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding, BUILD) if torch else None
+        if lib:
+            _link(list(ex.map(lambda s: _compile(s, BUILD), srcs)))
+        if binding:
+            _link_binding(binding.result())
+    if verbose and lib:
         for s in srcs:
             with open(os.path.join(BUILD, os.path.basename(s) + ".ptxas.txt")) as f:
                 sys.stdout.write(f.read())
