@@ -394,6 +394,19 @@ PyObject *q4_gated_(PyObject *const *a) {
   return wrap(H);
 }
 
+// Whether a tensor's elements are all those from its first address on, in any
+// order: the norm and the scaling take them as they lie (the gradient of a
+// weight given as W.t() is F x D in storage).
+bool dense(const Tensor &t) { return t.is_contiguous() || t.is_non_overlapping_and_dense(); }
+// Whether the elements of two dense tensors correspond as they lie.
+bool same_order(const Tensor &a, const Tensor &b) {
+  if (a.is_contiguous() && b.is_contiguous()) return a.numel() == b.numel();
+  if (a.sizes() != b.sizes()) return false;
+  for (int64_t d = 0; d < a.dim(); ++d)
+    if (a.size(d) > 1 && a.stride(d) != b.stride(d)) return false;
+  return true;
+}
+
 // grad_norm_clip(grads, outs, max_norm, stream, workspace); lists, outs may be None
 PyObject *grad_norm_clip_(PyObject *const *a) {
   if (!PyList_Check(a[0]) || (a[1] != Py_None && !PyList_Check(a[1])))
@@ -407,17 +420,17 @@ PyObject *grad_norm_clip_(PyObject *const *a) {
   int device = -1;
   for (Py_ssize_t i = 0; i < n; ++i) {
     const Tensor &t = tensor(PyList_GET_ITEM(a[0], i), "grads");
-    if (!t.is_cuda() || !t.is_contiguous() || (device >= 0 && t.get_device() != device))
-      refuse("grads must be contiguous CUDA tensors of one device");
+    if (!t.is_cuda() || !dense(t) || (device >= 0 && t.get_device() != device))
+      refuse("grads must be CUDA tensors of one device, dense in any order of their dimensions");
     device = t.get_device();
     dtypes[i] = dtype_code(t, "grads");
     in[i] = t.data_ptr();
     sizes[i] = t.numel();
     if (a[1] == Py_None) continue;
     const Tensor &o = tensor(PyList_GET_ITEM(a[1], i), "out");
-    if (!o.is_cuda() || !o.is_contiguous() || o.get_device() != device ||
-        o.scalar_type() != t.scalar_type() || o.numel() != t.numel())
-      refuse("out must match grads in sizes, dtypes and device, and be contiguous");
+    if (!o.is_cuda() || o.get_device() != device || o.scalar_type() != t.scalar_type() ||
+        !same_order(t, o))
+      refuse("out must match grads in sizes, dtypes, device and order of storage");
     out[i] = o.data_ptr();
   }
   const double max_norm = PyFloat_AsDouble(a[2]);

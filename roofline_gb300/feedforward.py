@@ -124,7 +124,9 @@ def grad_norm_workspace(count) -> int:
 
 def clip_grad_norm(grads, max_norm, out=None, stream=None, workspace=None):
     """Scales every tensor by min(1, max_norm / (norm + 1e-6)) and returns the
-    norm before clipping.  In place, or into the tensors ``out``."""
+    norm before clipping.  In place, or into the tensors ``out``.  Tensors are
+    dense in any order of their dimensions (as ``gated_ff_backward`` returns the
+    gradients of a weight passed as ``W.t()``); an ``out`` has its gradient's."""
     grads = list(grads)
     return (_module or _native()).grad_norm_clip(grads, grads if out is None else list(out),
                                                  max_norm, _handle(stream), workspace)

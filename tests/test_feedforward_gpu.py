@@ -835,3 +835,44 @@ def test_workspaces_that_are_none_are_refused(ff):
     assert float(a) == float(b)
     with pytest.raises(gemm.GemmError):
         ff.grad_norm(ts, workspace=ws[:8])
+
+
+@pytest.mark.parametrize("order", ["oi", "io"])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_clip_what_the_backward_pass_returns(ff, dt, order):
+    """The gradients of weights in either order of storage are clipped as they come: in
+    place, and into outputs of the same order; with a few other dense orders."""
+    X, Wg, Wu, dH = _case(8, 60, 50, 33, dt, order)
+    _, G, U = ff.gated_ff(X, Wg, Wu, save=True)
+    ts = list(ff.gated_ff_backward(dH, X, Wg, Wu, G, U))
+    cube = torch.randn(3, 5, 7).to(dt).cuda()
+    ts += [cube.permute(2, 0, 1), cube.clone().transpose(0, 2), cube[:, :1].contiguous().expand(3, 1, 7)]
+    torch.cuda.synchronize()
+    before = [t.clone() for t in ts]
+    outs = [torch.full_like(t, 9.0) for t in ts]
+    norm = ff.clip_grad_norm(ts, 0.5, out=outs)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ts, before))
+    _check_clip(before, outs, norm, 0.5)
+    norm2 = ff.clip_grad_norm(ts, 0.5)
+    torch.cuda.synchronize()
+    assert float(norm2) == float(norm) == float(ff.grad_norm(before))
+    assert all(torch.equal(a, b) for a, b in zip(ts, outs))
+
+
+def test_clip_refuses_what_is_not_dense(ff):
+    t = torch.randn(8, 6).cuda()
+    for bad in (t[:, :3], t[::2], t[:1].expand(8, 6), t[:, :1].expand(8, 6)):
+        with pytest.raises(ValueError):
+            ff.grad_norm([bad])
+        with pytest.raises(ValueError):
+            ff.clip_grad_norm([torch.zeros_like(t)[:, :bad.shape[1]].contiguous()], 1.0, out=[bad])
+    a, b = t.t(), torch.empty(6, 8, device="cuda")  # one size, two orders
+    with pytest.raises(ValueError):
+        ff.clip_grad_norm([a], 1.0, out=[b])
+    with pytest.raises(ValueError):
+        ff.clip_grad_norm([b], 1.0, out=[a])
+    with pytest.raises(ValueError):
+        ff.clip_grad_norm([a], 1.0, out=[t])
+    with pytest.raises(ValueError):
+        ff.clip_grad_norm([t], 1.0, out=[t.bfloat16()])
