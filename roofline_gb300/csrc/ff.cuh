@@ -26,41 +26,71 @@ __device__ __forceinline__ bf16 from_f32<bf16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
-// 1 / (1 + exp(-x)) with the fast exponential and quotient.  Its relative
-// error, 2^-22 and 2^-24 |x|, counts in act(g) times 1 - sigmoid, so what
-// reaches the result is under 1e-7 of max(|g|, 1): FP32's own rounding.
-__device__ __forceinline__ float sigmoid(float x) {
-  return __fdividef(1.0f, 1.0f + __expf(-x));
+// The activations are computed in FP32 for results of type T.  FP32 results
+// take expf and erfcf (2048 x 1024 x 2816 trained with GELU: 337 us, 328 with
+// erff, whose 2^-23 of 1 is all there is of the negative tail at g = -5).  For
+// BF16 ones, rounded to 2^-9, the fast exponential (2 + 1.2 |x| units of 2^-23
+// off) and 1 + erf are enough.  The quotient, of a divisor from 1 to 2, is the
+// fast one in both, 2 units of 2^-23 off (rounded, 1023 x 777 x 1025 in FP32
+// takes 28.8 us instead of 27.2).
+template <typename T>
+__device__ __forceinline__ float exp_for(float x) {
+  return std::is_same<T, float>::value ? expf(x) : __expf(x);
+}
+
+// s = 1 / (1 + exp(-x)) and c = 1 - s, each with the relative accuracy of the
+// exponential, by e = exp(-|x|) <= 1: neither tail cancels or leaves the range
+// before the result itself does.
+struct Logistic {
+  float s, c;
+};
+template <typename T>
+__device__ __forceinline__ Logistic logistic(float x) {
+  const float e = exp_for<T>(-fabsf(x));
+  const float r = __fdividef(1.0f, 1.0f + e);
+  return x >= 0.0f ? Logistic{r, e * r} : Logistic{e * r, r};
+}
+
+// (1 + erf(g / sqrt(2))) / 2.  In FP32 by erfc, which keeps the negative tail.
+template <typename T>
+__device__ __forceinline__ float normal_cdf(float g) {
+  return std::is_same<T, float>::value ? 0.5f * erfcf(g * -0.70710678f)
+                                       : 0.5f * (1.0f + erff(g * 0.70710678f));
+}
+
+// (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u)), u as in the header's GELU_TANH.
+template <typename T>
+__device__ __forceinline__ Logistic tanh_gate(float g) {
+  return logistic<T>(2.0f * 0.79788456f * (g + 0.044715f * g * g * g));
 }
 
 // act(g) (formulas in gb300_gemm.h).
-template <int ACT>
+template <typename T, int ACT>
 __device__ __forceinline__ float act_of(float g) {
-  if (ACT == GEMM_ACT_SILU) return g * sigmoid(g);
+  if (ACT == GEMM_ACT_SILU) return g * logistic<T>(g).s;
   if (ACT == GEMM_ACT_RELU) return g > 0.0f ? g : (g != g ? g : 0.0f);
-  if (ACT == GEMM_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678f));
-  // (1 + tanh(u)) / 2 = sigmoid(2u)
-  return g * sigmoid(2.0f * 0.79788456f * (g + 0.044715f * g * g * g));
+  if (ACT == GEMM_ACT_GELU) return g * normal_cdf<T>(g);
+  return g * tanh_gate<T>(g).s;
 }
 
 // act(g) and act'(g).
-template <int ACT>
+template <typename T, int ACT>
 __device__ __forceinline__ void act_both(float g, float &a, float &d) {
   if (ACT == GEMM_ACT_SILU) {
-    const float s = sigmoid(g);
-    a = g * s;
-    d = s * (1.0f + g * (1.0f - s));
+    const Logistic l = logistic<T>(g);
+    a = g * l.s;
+    d = l.s * (1.0f + g * l.c);
   } else if (ACT == GEMM_ACT_RELU) {
-    a = act_of<ACT>(g);
+    a = act_of<T, ACT>(g);
     d = g > 0.0f ? 1.0f : 0.0f;
   } else if (ACT == GEMM_ACT_GELU) {
-    const float p = 0.5f * (1.0f + erff(g * 0.70710678f));
+    const float p = normal_cdf<T>(g);
     a = g * p;
-    d = p + g * 0.39894228f * __expf(-0.5f * g * g);
+    d = p + g * 0.39894228f * exp_for<T>(-0.5f * g * g);
   } else {
-    const float s = sigmoid(2.0f * 0.79788456f * (g + 0.044715f * g * g * g));
-    a = g * s;
-    d = s + 2.0f * g * s * (1.0f - s) * 0.79788456f * (1.0f + 0.134145f * g * g);
+    const Logistic l = tanh_gate<T>(g);
+    a = g * l.s;
+    d = l.s + 2.0f * g * l.s * l.c * 0.79788456f * (1.0f + 0.134145f * g * g);
   }
 }
 

@@ -50,7 +50,7 @@ __device__ __forceinline__ void finish(const FewArgs &p, int64_t m, int64_t n, f
     p.g[m * p.ldg + n] = s0;
     p.u[m * p.ldu + n] = s1;
   }
-  if (p.c) with_act(p.act, [&](auto a) { p.c[m * p.ldc + n] = act_of<decltype(a)::value>(s0) * s1; });
+  if (p.c) with_act(p.act, [&](auto a) { p.c[m * p.ldc + n] = act_of<float, decltype(a)::value>(s0) * s1; });
 }
 
 // b0, b1: N rows of K.  Two rows of each a warp; `split` warps of a block share

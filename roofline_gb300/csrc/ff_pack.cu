@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256) ff_dgate_kernel(GateAndPack q) {
     load8(p.u + r * p.ldu, c, p.F, vu, u);
     with_act(p.act, [&](auto act) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) act_both<decltype(act)::value>(g[i], a[i], d[i]);
+      for (int i = 0; i < 8; ++i) act_both<T, decltype(act)::value>(g[i], a[i], d[i]);
     });
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -288,7 +288,7 @@ struct Writer {
   __device__ __forceinline__ void combine(float (&x)[8], const float (&y)[8]) const {
     with_act(act, [&](auto a) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = act_of<decltype(a)::value>(x[i]) * y[i];
+      for (int i = 0; i < 8; ++i) x[i] = act_of<T, decltype(a)::value>(x[i]) * y[i];
     });
   }
 

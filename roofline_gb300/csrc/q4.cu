@@ -649,7 +649,7 @@ q4_kernel(const Q4Args p) {
     }
     if (!here) continue;
     if constexpr (GATED)
-      with_act(p.act, [&](auto a) { y = act_of<decltype(a)::value>(y) * u; });
+      with_act(p.act, [&](auto a) { y = act_of<T, decltype(a)::value>(y) * u; });
     static_cast<T *>(p.y)[(m0 + m) * p.ldy + n0 + r] = from_f32<T>(y);
   }
   if (p.split > 1) cluster_sync();  // the others have read this CTA's sums

@@ -876,3 +876,86 @@ def test_clip_refuses_what_is_not_dense(ff):
         ff.clip_grad_norm([a], 1.0, out=[t])
     with pytest.raises(ValueError):
         ff.clip_grad_norm([t], 1.0, out=[t.bfloat16()])
+
+
+# ------------------------------------------------------------------ the activations' tails
+
+def _act64(g, act):
+    """act and act' in 64 bits with the accuracy of their tails, and how far FP32 rounding of
+    the exponent's argument moves each, relative (2^-23 of the argument)."""
+    g = g.double()
+    if act == "silu":
+        s, c, arg = torch.sigmoid(g), torch.sigmoid(-g), torch.zeros_like(g)
+        return g * s, s + g * s * c, (s + (g * s * c).abs()), arg
+    if act == "gelu":
+        p = 0.5 * torch.erfc(-g * math.sqrt(0.5))
+        f = torch.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
+        return g * p, p + g * f, p + (g * f).abs(), g * g
+    k = math.sqrt(2 / math.pi)
+    u = 2 * k * (g + 0.044715 * g ** 3)
+    s, c = torch.sigmoid(u), torch.sigmoid(-u)
+    t = 2 * g * s * c * k * (1 + 0.134145 * g * g)
+    return g * s, s + t, s + t.abs(), u.abs()
+
+
+def _tail_points(act, limit):
+    """Gate values of both signs from 1e-3 on to where act's negative tail passes `limit`."""
+    top = {"silu": math.log(limit) * -1.06, "gelu": math.sqrt(-2 * math.log(limit)),
+           "gelu_tanh": (-math.log(limit) / 0.0713) ** (1 / 3)}[act]
+    g = torch.logspace(-3, math.log10(top), 150)
+    g = torch.cat((g, -g))
+    return g[_act64(g, act)[0].abs() >= limit]
+
+
+@pytest.mark.parametrize("M", [4, 64])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_activation_tails(ff, dt, act, M):
+    """H = act(G) for G as given (a width of 2, U = 1), relative to act(G) itself down to where
+    it leaves the normal numbers.  FP32: erfcf and expf within 4 units of 2^-23, a quotient,
+    sums and two products within 4 more, and the argument's rounding, which the
+    exponential multiplies: 3 of 2^-23.  BF16: the fast exponential, 2 + 1.2 |x| of 2^-23, and
+    the rounding of the result; erf's 2^-23 is of 1, not of its tail."""
+    points = _tail_points(act, 2.0 ** -125).to(dt)
+    n = -(-points.numel() // M) * M
+    g = torch.cat((points, points[:1].expand(n - points.numel()))).view(M, -1)
+    F = g.shape[1]
+    for j in range(F):  # one column of gates a call: G(m, j) = X(m, 0)
+        X = torch.ones((M, 2), dtype=dt)
+        X[:, 0] = g[:, j]
+        Wg, Wu = torch.zeros((2, 1), dtype=dt), torch.zeros((2, 1), dtype=dt)
+        Wg[0], Wu[1] = 1.0, 1.0
+        X, Wg, Wu = X.cuda(), Wg.cuda(), Wu.cuda()
+        H, G, U = ff.gated_ff(X, Wg, Wu, act=act, save=True)
+        torch.cuda.synchronize()
+        assert torch.equal(G, X[:, :1].float()) and bool((U == 1).all())
+        want, _, _, arg = _act64(g[:, j], act)
+        if dt == F32:
+            tol = (8 + 3 * arg) * 2.0 ** -23 * want.abs()
+        else:
+            e = arg if act == "gelu_tanh" else g[:, j].double().abs()
+            tol = want.abs() * (2.0 ** -8 + (8 + 6 * e) * 2.0 ** -23)
+            if act == "gelu":
+                tol = tol + g[:, j].double().abs() * 2.0 ** -23
+        assert bool(((H[:, 0].double().cpu() - want).abs() <= tol + 2.0 ** -133).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activation_gradient_tails_f32(ff, act):
+    """dX of a width of 2 with Wg = (1, 0), Wu = (0, 1), dH = U = 1 is (act'(G), act(G)): the
+    bound of act for each term of act', relative to the terms."""
+    points = _tail_points(act, 2.0 ** -110)
+    n = -(-points.numel() // 16) * 16
+    g = torch.cat((points, points[:1].expand(n - points.numel()))).view(16, -1)
+    Wg, Wu = torch.zeros((2, 1)).cuda(), torch.zeros((2, 1)).cuda()
+    Wg[0], Wu[1] = 1.0, 1.0
+    one = torch.ones((16, 1)).cuda()
+    for j in range(g.shape[1]):
+        dX, _, _ = ff.gated_ff_backward(one, torch.ones((16, 2)).cuda(), Wg, Wu,
+                                        g[:, j:j + 1].cuda(), one, act=act, need_dw=False)
+        torch.cuda.synchronize()
+        a, d, terms, arg = _act64(g[:, j], act)
+        tol = (12 + 3 * arg) * 2.0 ** -23
+        got = dX.double().cpu()
+        assert bool(((got[:, 0] - d).abs() <= tol * terms + 2.0 ** -140).all())
+        assert bool(((got[:, 1] - a).abs() <= tol * a.abs() + 2.0 ** -140).all())
