@@ -90,7 +90,8 @@ __device__ __forceinline__ void act_both(float g, float &a, float &d) {
   } else {
     const Logistic l = tanh_gate<T>(g);
     a = g * l.s;
-    d = l.s + 2.0f * g * l.s * l.c * 0.79788456f * (1.0f + 0.134145f * g * g);
+    // s c is 0 long before g g leaves FP32's range, where their product would be NaN
+    d = l.s + l.s * l.c * (1.59576912f * (1.0f + 0.134145f * fminf(g * g, 1e30f))) * g;
   }
 }
 

@@ -959,3 +959,21 @@ def test_activation_gradient_tails_f32(ff, act):
         got = dX.double().cpu()
         assert bool(((got[:, 0] - d).abs() <= tol * terms + 2.0 ** -140).all())
         assert bool(((got[:, 1] - a).abs() <= tol * a.abs() + 2.0 ** -140).all())
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_activations_of_huge_gates(ff, dt, act):
+    """Gates whose square or cube leaves FP32's range, up to its end: act is g or 0, act' 1 or
+    0, exactly (the exponential is 0, erf 1)."""
+    g = torch.tensor([1e6, 1e13, 3e19, 1e25, 3e38])
+    g = torch.cat((g, -g))[:, None].cuda()
+    n = g.shape[0]
+    Wg, Wu = torch.zeros((2, 1), dtype=dt).cuda(), torch.zeros((2, 1), dtype=dt).cuda()
+    Wg[0], Wu[1] = 1.0, 1.0
+    X = torch.ones((n, 2), dtype=dt, device="cuda")
+    dX, _, _ = ff.gated_ff_backward(X[:, :1].contiguous(), X, Wg, Wu, g, torch.ones_like(g),
+                                    act=act, need_dw=False)
+    torch.cuda.synchronize()
+    assert torch.equal(dX[:, 0], (g[:, 0] > 0).to(dt))
+    assert torch.equal(dX[:, 1], torch.clamp(g[:, 0], min=0).to(dt))
