@@ -213,6 +213,11 @@ uint64_t block_bytes(int backward, int dtype, int op, int64_t M, int64_t D, int6
   // sizes that it refuses the call itself refuses too
   return gated_ff_workspace(backward, dtype, op, M, D, F, aligned, &need) == GEMM_OK ? need : 0;
 }
+// A tensor that a call has written: autograd is to know that what it may have
+// kept of it is no longer there.
+void written(const Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 void *address(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 PyObject *wrap(const Tensor &t) {
   if (t.defined()) return THPVariable_Wrap(t);
@@ -269,6 +274,7 @@ PyObject *gated_ff_(PyObject *const *a) {
                     wu.data_ptr(), u.ld[op], H.data_ptr(), ldh, static_cast<float *>(address(G)),
                     lds, static_cast<float *>(address(U)), lds, ws.p, ws.bytes, s);
   });
+  if (a[5] != Py_None) written(H);
   return save ? triple(H, G, U) : wrap(H);
 }
 
@@ -365,6 +371,7 @@ PyObject *q4_matmul_(PyObject *const *a) {
     return q4_matmul(x.dtype, x.rows, N, x.cols, x.t.data_ptr(), x.ld, w.q.data_ptr(), w.ldq,
                      w.s.data_ptr(), w.z, (int)group, Y.data_ptr(), ldy, s);
   });
+  if (a[5] != Py_None) written(Y);
   return wrap(Y);
 }
 
@@ -391,6 +398,7 @@ PyObject *q4_gated_(PyObject *const *a) {
                     g.s.data_ptr(), g.z, u.q.data_ptr(), u.ldq, u.s.data_ptr(), u.z, (int)group,
                     H.data_ptr(), ldh, s);
   });
+  if (a[9] != Py_None) written(H);
   return wrap(H);
 }
 
@@ -448,6 +456,8 @@ PyObject *grad_norm_clip_(PyObject *const *a) {
                           sizes.data(), (float)max_norm, static_cast<float *>(norm.data_ptr()),
                           ws.p, ws.bytes, s);
   });
+  if (a[1] != Py_None)
+    for (Py_ssize_t i = 0; i < n; ++i) written(THPVariable_Unpack(PyList_GET_ITEM(a[1], i)));
   return wrap(norm);
 }
 

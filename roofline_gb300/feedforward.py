@@ -13,6 +13,9 @@ with torch's own operators its order with the streams that made the inputs, or
 that use the outputs, is the caller's part; new outputs are of the given
 stream's memory, so nothing before the call uses them.
 
+No call records a graph for autograd: outputs require no gradient, whatever the
+inputs do.  What is written in place or into ``out`` counts as modified.
+
 ``workspace``: optional contiguous CUDA tensor used as scratch
 (``gated_ff_workspace`` or ``grad_norm_workspace`` bytes, which no other work
 uses at the time).  Without one a call takes its own from torch's allocator, on

@@ -977,3 +977,34 @@ def test_activations_of_huge_gates(ff, dt, act):
     torch.cuda.synchronize()
     assert torch.equal(dX[:, 0], (g[:, 0] > 0).to(dt))
     assert torch.equal(dX[:, 1], torch.clamp(g[:, 0], min=0).to(dt))
+
+
+def test_tensors_written_in_place_count_as_modified(ff):
+    """Autograd refuses to use a saved tensor that a call has written since; the version of
+    what a call only reads stays."""
+    X, Wg, Wu, _ = _case(7, 20, 16, 24, F32, "io")
+    q, s, _ = _quant(torch.Generator().manual_seed(1), 24, 16, 32, F32, False)
+    outs = [torch.zeros((20, 24), device="cuda") for _ in range(3)]
+    for out, call in zip(outs, (
+            lambda o: ff.gated_ff(X, Wg, Wu, out=o), lambda o: ff.q4_matmul(X, q, s, group=32, out=o),
+            lambda o: ff.q4_gated(X, q, s, q, s, group=32, out=o))):
+        x = torch.ones((20, 24), device="cuda", requires_grad=True)
+        y = (x * out).sum()  # keeps `out` for the gradient of x
+        before = out._version
+        assert call(out) is out and out._version > before
+        with pytest.raises(RuntimeError, match="modified"):
+            y.backward()
+    grads = [torch.ones(100, device="cuda"), torch.ones(7, device="cuda")]
+    dest = [torch.ones(100, device="cuda"), torch.ones(7, device="cuda")]
+    versions = [t._version for t in (X, Wg, q, s, *grads)]
+    ff.grad_norm(grads)
+    ff.clip_grad_norm(grads, 1.0, out=dest)
+    assert versions == [t._version for t in (X, Wg, q, s, *grads)]
+    assert all(t._version > 0 for t in dest)
+    ff.clip_grad_norm(grads, 1.0)
+    assert all(t._version > v for t, v in zip(grads, versions[-2:]))
+    with torch.inference_mode():
+        t = torch.ones(100, device="cuda")
+        ff.clip_grad_norm([t], 1.0)
+        assert abs(float(t.norm()) - 1.0) < 1e-5
+    torch.cuda.synchronize()
