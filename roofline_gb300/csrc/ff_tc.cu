@@ -892,7 +892,15 @@ int launch_cfg(const FfProduct *q, int n, const Choice *ch, const DeviceProps &d
     l.early = (int64_t)(clocks[0] / clocks[1]);
     if (l.early > share) l.early = share;
   }
-  l.wait_ns = env_u64("GEMM_DEBUG_WAIT_LIMIT_NS", 2000000000ull);
+  // The epilogue's one wait is for a whole sum, 0.3 us a block of K in BF16 (2 s
+  // alone would end sums over 4.7e8 tokens), and the pair's other CTA may be a
+  // block of FP32, 2 us, behind: the limit grows with the sum.
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t k = (int64_t)l.p[i].kb * l.p[i].segs;
+    if (k > blocks) blocks = k;
+  }
+  l.wait_ns = env_u64("GEMM_DEBUG_WAIT_LIMIT_NS", 2000000000ull) + (uint64_t)blocks * 8000;
   l.stall_producer = (int)env_u64("GEMM_DEBUG_STALL_PRODUCER", 0);
 
   auto kern = ff_tc_kernel<P, CG, BN, GATED>;

@@ -311,6 +311,22 @@ def test_stalled_pipeline_reports_timeout(ff, size, monkeypatch):
     assert gemm.check_status() == gemm.OK
 
 
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_wait_limit_grows_with_the_sum(ff, dt, monkeypatch):
+    """A sum that takes longer than the limit of a short wait (here 0.1 ms, for 4096 blocks of
+    K of 0.2 us each or more) is not taken for a stalled one."""
+    from roofline_gb300 import gemm
+    M, D, F = 40, 1 << 18, 64
+    X, Wg, Wu, _ = _case(5, M, D, F, dt, "oi")
+    want = ff.gated_ff(X, Wg, Wu)
+    assert gemm.check_status() == gemm.OK
+    with monkeypatch.context() as m:
+        m.setenv("GEMM_DEBUG_WAIT_LIMIT_NS", "100000")
+        got = ff.gated_ff(X, Wg, Wu)
+        assert gemm.check_status() == gemm.OK
+    assert torch.equal(got, want)
+
+
 # ------------------------------------------------------------------ 4-bit products
 
 def _quant(g, N, K, group, dt, zeros, pad=0):
