@@ -15,7 +15,8 @@
 // sum is 2^-8 of the result and its rounding as much smaller, gather in a
 // second accumulator over the whole of K.  The small products of a K block
 // take five times as long as x_0 y_0, and the registers are updated
-// meanwhile, so the MMAs never wait for it.
+// meanwhile, so the MMAs never wait for it.  A BF16 product's sum is one
+// accumulator's up to 32768 of K; longer ones are added up in parts (kLong).
 //
 // GB300 (a dense BF16 GEMM reaches 1920 TFLOP/s in a burst, 1725 sustained):
 // BF16 4096 x 4096 x 14336, 0.96 TFLOP, 507-524 us, the tensor pipe busy 87 %
@@ -40,6 +41,10 @@ __device__ int g_ff_status;  // 0 = ok, else a GEMM_ERR_* code
 constexpr int kThreadsFF = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kFlush = 4;
+// K blocks of one part of a long BF16 sum.  The rounding towards zero takes up
+// to 1.6 x 2^-24 of a sum of one sign for every 16 of K: 1.5e-4 over a part's
+// 32768, a thirteenth of BF16's own rounding, but 6e-3 over a million tokens.
+constexpr int kLong = 512;
 
 // One product of a launch.
 struct FfParams {
@@ -266,6 +271,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
       : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&r)[16]) {
+  uint32_t v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(r[i]);
+  tmem_st<16>(taddr, v);
+}
+
 // What a warp's blocks of 32 rows x 16 columns become: c = v, or (gated)
 // act(v) * w with v and w themselves to g and u if given.
 template <typename T, bool GATED>
@@ -383,6 +395,31 @@ struct Writer {
   }
 };
 
+// One part of a long sum: the columns of this warp's blocks (every second 16 from
+// j0 on, gated: of both sums) at `from`, with those at `sum` if they are to be
+// added, to `to`.
+template <bool GATED>
+__device__ __forceinline__ void gather_part(uint32_t from, uint32_t sum, uint32_t to, bool add,
+                                         int out_cols, int j0) {
+#pragma unroll 1
+  for (int j = j0; j < out_cols; j += 32) {
+#pragma unroll
+    for (int side = 0; side < (GATED ? 2 : 1); ++side) {
+      const uint32_t at = (uint32_t)(side * out_cols + j);
+      float v[16], w[16];
+      tmem_ld16(from + at, v);
+      if (add) tmem_ld16(sum + at, w);
+      tmem_ld_wait();
+      if (add) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] += w[k];
+      }
+      tmem_st16(to + at, v);
+    }
+  }
+  tmem_st_wait();
+}
+
 struct TileAt {
   int64_t m, n;
   int batch;
@@ -403,11 +440,14 @@ __device__ __forceinline__ TileAt tile_at(const FfParams &p, int64_t t) {
 // CG: CTAs that share one tile of CG * 128 rows (a pair splits the columns of
 // B between its two shared memories).  BN: accumulator columns of a tile, of
 // which the gated form gives half to each of its two sums; with one plane it
-// is chosen at run time (BN = 0).  P: planes.
-template <int P, int CG, int BN, bool GATED>
+// is chosen at run time (BN = 0).  P: planes.  LONG: one plane, sums over more
+// than kLong blocks among the launch's; apart, because what they need in the
+// issuing thread's and the epilogue's loops slows the other sums down by 2 %
+// (4096 x 4096 x 14336 590 -> 602 us, 1025 x 777 x 1341 trained 52.8 -> 54.0).
+template <int P, int CG, int BN, bool GATED, bool LONG>
 __global__ void __launch_bounds__(kThreadsFF, 1)
 ff_tc_kernel(const __grid_constant__ FfLaunch l) {
-  static_assert((P == 1) == (BN == 0), "");
+  static_assert((P == 1) == (BN == 0) && (P == 1 || !LONG), "");
   using T = typename std::conditional<P == 1, bf16, float>::type;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -548,6 +588,10 @@ ff_tc_kernel(const __grid_constant__ FfLaunch l) {
           if (!take(acc)) break;
         }
         for (int kb = 0; kb < kbs; ++kb) {
+          if (LONG && kb > 0 && kb % kLong == 0) {
+            commit<CG>(&acc_full[acc]);
+            if (!take(acc)) break;
+          }
           if (!ff_wait(&full[s], ph, l.wait_ns, abort_flag)) {
             ok = false;
             break;
@@ -560,7 +604,7 @@ ff_tc_kernel(const __grid_constant__ FfLaunch l) {
             if (!take(acc)) break;
           }
           const uint32_t d = tmem_base + (uint32_t)(acc * A::COLS);
-          const bool first = P == 1 ? kb == 0 : kb % kFlush == 0;
+          const bool first = LONG ? kb % kLong == 0 : P == 1 ? kb == 0 : kb % kFlush == 0;
 #pragma unroll
           for (int kk = 0; kk < kBlockK / 16; ++kk)
             mma_bf16<CG>(d, da + kk * astep, db + kk * bstep, idesc, first && kk == 0 ? 0u : 1u);
@@ -584,6 +628,7 @@ ff_tc_kernel(const __grid_constant__ FfLaunch l) {
           if (++s == stages) s = 0, ph ^= 1;
         }
         if (ok) commit<CG>(&acc_full[P == 1 ? acc : A::SMALL]);
+        if (LONG && kbs > kLong) acc ^= 1;  // the other one holds the sum of the parts
       }
     }
   } else {
@@ -635,8 +680,23 @@ ff_tc_kernel(const __grid_constant__ FfLaunch l) {
       out.u = p.u ? p.u + r0 * p.ldu : nullptr;
       if constexpr (P == 1) {
         acc ^= 1;
-        if (!wait_full(acc)) break;
         const uint32_t base = lane_base + (uint32_t)(acc * A::COLS);
+        // A long sum comes in parts, which gather in the place of the accumulator
+        // that the tile before this one had: this warp has read its share of it,
+        // and the MMAs go on in the one that it reads last here.
+        const int parts = LONG ? (p.kb * p.segs + kLong - 1) / kLong : 1;
+        if (!wait_full(acc)) break;
+        if constexpr (LONG) {
+          const uint32_t sum = lane_base + (uint32_t)((acc ^ 1) * A::COLS);
+          for (int part = 0; parts > 1; ++part) {
+            const bool last = part == parts - 1;
+            gather_part<GATED>(base, sum, last ? base : sum, part > 0, out_cols, 16 * half);
+            if (last) break;
+            release(acc);
+            if (!wait_full(acc)) break;
+          }
+          if (!ok) break;
+        }
         int j = 16 * half;
         if (j >= out_cols) release(acc);
 #pragma unroll 1
@@ -648,6 +708,7 @@ ff_tc_kernel(const __grid_constant__ FfLaunch l) {
           if (j + 32 >= out_cols) release(acc);
           out.block(c0 + j, v, w);
         }
+        if (LONG && parts > 1) acc ^= 1;
       } else {
         constexpr int COLS = GATED ? BN / 4 : BN / 2;  // output columns of a warp
         constexpr int BLOCKS = BN / 32;                // 16 columns of the sums each
@@ -861,7 +922,7 @@ void choose(const FfProduct *q, int n, int sms, Choice *best) {
   }
 }
 
-template <int P, int CG, int BN, bool GATED>
+template <int P, int CG, int BN, bool GATED, bool LONG>
 int launch_cfg(const FfProduct *q, int n, const Choice *ch, const DeviceProps &dp,
                cudaStream_t s) {
   FfLaunch l{};
@@ -903,7 +964,7 @@ int launch_cfg(const FfProduct *q, int n, const Choice *ch, const DeviceProps &d
   l.wait_ns = env_u64("GEMM_DEBUG_WAIT_LIMIT_NS", 2000000000ull) + (uint64_t)blocks * 8000;
   l.stall_producer = (int)env_u64("GEMM_DEBUG_STALL_PRODUCER", 0);
 
-  auto kern = ff_tc_kernel<P, CG, BN, GATED>;
+  auto kern = ff_tc_kernel<P, CG, BN, GATED, LONG>;
   static Once once;
   if (allow_shared_memory(once, kern, 227 * 1024, dp.device) != cudaSuccess) {
     cudaGetLastError();
@@ -934,15 +995,21 @@ int launch_any(const FfProduct *q, int n, const DeviceProps &dp, cudaStream_t s)
   Choice c[2];
   choose(q, n, dp.sm_count, c);
   if constexpr (P == 1) {
-    return c[0].cg == 2 ? launch_cfg<1, 2, 0, GATED>(q, n, c, dp, s)
-                        : launch_cfg<1, 1, 0, GATED>(q, n, c, dp, s);
+    bool is_long = false;
+    for (int i = 0; i < n; ++i)
+      is_long = is_long || ceil_div(q[i].K, kBlockK) * (q[i].kind == kFfConcat ? 2 : 1) > kLong;
+    if (is_long)
+      return c[0].cg == 2 ? launch_cfg<1, 2, 0, GATED, true>(q, n, c, dp, s)
+                          : launch_cfg<1, 1, 0, GATED, true>(q, n, c, dp, s);
+    return c[0].cg == 2 ? launch_cfg<1, 2, 0, GATED, false>(q, n, c, dp, s)
+                        : launch_cfg<1, 1, 0, GATED, false>(q, n, c, dp, s);
   } else {
     if (c[0].cg == 2)
-      return c[0].bn == 256 ? launch_cfg<3, 2, 256, GATED>(q, n, c, dp, s)
-                            : launch_cfg<3, 2, 128, GATED>(q, n, c, dp, s);
+      return c[0].bn == 256 ? launch_cfg<3, 2, 256, GATED, false>(q, n, c, dp, s)
+                            : launch_cfg<3, 2, 128, GATED, false>(q, n, c, dp, s);
     if constexpr (!GATED)
-      if (c[0].bn == 64) return launch_cfg<3, 1, 64, false>(q, n, c, dp, s);
-    return launch_cfg<3, 1, 128, GATED>(q, n, c, dp, s);
+      if (c[0].bn == 64) return launch_cfg<3, 1, 64, false, false>(q, n, c, dp, s);
+    return launch_cfg<3, 1, 128, GATED, false>(q, n, c, dp, s);
   }
 }
 

@@ -311,6 +311,53 @@ def test_stalled_pipeline_reports_timeout(ff, size, monkeypatch):
     assert gemm.check_status() == gemm.OK
 
 
+@pytest.mark.parametrize("order", ["oi", "io"])
+@pytest.mark.parametrize("size", [(70, 70000, 200), (300, 33000, 1100), (1, 32800, 40),
+                                  (40000, 72, 130), (70000, 40, 300), (130, 100, 20000),
+                                  (300, 600, 16400)])
+def test_long_sums_bf16(ff, size, order):
+    """Sums longer than an accumulator keeps, of the block (one CTA a tile and pairs), of dX
+    and of dW, and launches whose other product's sums are short: the bounds of short ones,
+    and equal bits on repeat."""
+    from roofline_gb300 import gemm
+    X, Wg, Wu, dH = _case(sum(size), *size, BF16, order)
+    G, U = _check_forward(ff, X, Wg, Wu, "silu")
+    _check_backward(ff, dH, X, Wg, Wu, G, U, "silu")
+    H = ff.gated_ff(X, Wg, Wu)
+    grads = ff.gated_ff_backward(dH, X, Wg, Wu, G, U)
+    for _ in range(5):
+        assert torch.equal(ff.gated_ff(X, Wg, Wu), H)
+        for a, b in zip(ff.gated_ff_backward(dH, X, Wg, Wu, G, U), grads):
+            assert torch.equal(a, b)
+    assert gemm.check_status() == gemm.OK
+
+
+@pytest.mark.parametrize("K", [32768, 32769, 90000, 400000])
+def test_long_sums_of_one_sign_bf16(ff, K):
+    """Products of one sign, where every rounding towards zero has the same sign: however
+    long, a sum is off by no more than a part of 32768 is.  An MMA adds 16 of K by at most two
+    roundings of 2^-23 to a sum that grows evenly: 2^-12 over 2048 of them.  Parts are
+    added in FP32, 2^-24 each."""
+    g = torch.Generator().manual_seed(K)
+    tol = 2.0 ** -12 + (K // 32768 + 1) * 2.0 ** -24
+    X = (torch.rand((40, K), generator=g) + 0.5).to(BF16).cuda()
+    Wg = (torch.rand((24, K), generator=g) + 0.5).to(BF16).cuda().t()
+    _, G, U = ff.gated_ff(X, Wg, Wg, act="relu", save=True)
+    want = X.double() @ Wg.double()
+    assert bool(((G.double() - want).abs() <= tol * want).all()) and torch.equal(G, U)
+    # dW over K tokens, dG = dU = dH exactly
+    X, dH = X.t()[:, :16].contiguous(), X.t()[:, 16:32].contiguous()
+    one = torch.ones((K, 16), device="cuda")
+    W = torch.ones((16, 16), dtype=BF16, device="cuda")
+    _, dWg, dWu = ff.gated_ff_backward(dH, X, W, W, one, one, act="relu", need_dx=False)
+    want = X.double().t() @ dH.double()
+    torch.cuda.synchronize()
+    # rounding keeps the order: the result lies between the rounded ends of what the sum may be
+    low, high = ((want * (1 + d)).float().to(BF16) for d in (-tol, tol))
+    assert bool(((dWg >= low) & (dWg <= high)).all())
+    assert torch.equal(dWg, dWu)
+
+
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_wait_limit_grows_with_the_sum(ff, dt, monkeypatch):
     """A sum that takes longer than the limit of a short wait (here 0.1 ms, for 4096 blocks of
