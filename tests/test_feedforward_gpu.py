@@ -408,6 +408,21 @@ def test_q4(ff, size, dt, zeros, group):
 
 
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M", [64, 100, 257, 1000])
+@pytest.mark.parametrize("N,K", [(70, 513), (300, 2048)])
+def test_q4_many_tokens(ff, N, K, M, dt):
+    """Prompts: many passes over the weights, the last one not full."""
+    g = torch.Generator().manual_seed(N + M)
+    X = _mat(g, M, K, dt)
+    w, u = _quant(g, N, K, 128, dt, True), _quant(g, N, K, 128, dt, True)
+    Y = ff.q4_matmul(X, w[0], w[1], zeros=w[2], group=128)
+    H = ff.q4_gated(X, w[0], w[1], u[0], u[1], zeros_g=w[2], zeros_u=u[2], group=128, act="gelu")
+    torch.cuda.synchronize()
+    assert ref.worst(Y, ref.q4_rounded(X, *w, 128)) <= 1.0
+    assert ref.worst(H, ref.q4_gated(X, w, u, 128, "gelu")) <= 1.0
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("M", [1, 3, 16, 19])
 @pytest.mark.parametrize("N,K", [(5, 20000), (33, 12345), (200, 8192), (1000, 8200), (3000, 4104)])
 def test_q4_few_rows_long_sums(ff, N, K, M, dt):
