@@ -345,8 +345,8 @@ extern "C" int gated_ff_backward(int dtype, int act, int op_w, int64_t M, int64_
   const cudaError_t e = launch_dgate(gate, lay.jobs, lay.n, dtype, dp.sm_count, stream);
   if (e != cudaSuccess) return to_status(e);
   if (!dX || !dWg) return launch_ff_products(dX ? &px : &pw, 1, dp, stream);
-  // Both in one launch: the tiles that do not fill a wave of one product are
-  // followed by the other's.  Apart / merged with the gate's pass, us: BF16
+  // Both in one launch, always: the tiles that do not fill a wave of one product
+  // are followed by the other's, which pays in all of these but one.  Apart / merged with the gate's pass, us: BF16
   // 2048 x 1024 x 2816 91 / 55, 1024 x 1024 x 2816 62 / 57, 4096 x 4096 x 11008
   // 1112 / 1035, 8192 x 4096 x 11008 2137 / 2069, 1024 x 4096 x 11008 (weights
   // D x F) 299 / 319; FP32 2048 x 1024 x 2816 271 / 199.

@@ -20,9 +20,9 @@
 //
 // GB300 (a dense BF16 GEMM reaches 1920 TFLOP/s in a burst, 1725 sustained):
 // BF16 4096 x 4096 x 14336, 0.96 TFLOP, 507-524 us, the tensor pipe busy 87 %
-// of it; 1 x 4096 x 11008, 180 MB, 32.9 us (5.5 TB/s).  FP32 2048 x 1024 x 2816:
-// the block 116 us with the tensor pipe 66 % busy (142 GFLOP of BF16 products:
-// 74 us), its gradients 164 us, 87 % busy.
+// of it; 1 x 4096 x 11008, 180 MB, 32.9 us (5.5 TB/s).  FP32 2048 x 1024 x 2816
+// with GELU: the block 125 us with the tensor pipe 60 % busy (142 GFLOP of BF16
+// products: 74 us), its gradients 165 us, 86 % busy.
 #include <cstdlib>
 #include <mutex>
 

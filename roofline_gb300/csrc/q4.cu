@@ -7,7 +7,9 @@
 // their use, asynchronously, 128 bytes of a row at a time, with no barrier between
 // warps; and the arithmetic per code is kept small: a 32-bit word of eight codes becomes four BF16 pairs
 // 128 + q, exact, by 3 shifts and 4 three-input logic operations that mask and
-// or in the exponent of 128.
+// or in the exponent of 128 (integers put under the exponent of a float whose
+// last place is 1; Kim et al., "Who Says Elephants Can't Run", 2022, have it for
+// 4-bit weights).
 //
 // GB300, from cold caches, BF16, groups of 128: 1 token by 2 x 14336 x 4096
 // (60.6 MB) 20.7 us, 2.9 TB/s, the ALU pipe 50 % and the issue slots 49 %
@@ -15,7 +17,7 @@
 // both sides.  16 tokens by 8192 x 28672 (132 MB) 61.5 us, 2.1 TB/s: without
 // the copies 49, without x's loads 55, the copies alone 29; the arithmetic is
 // no faster with 16 warps (MMA and ALU work add up).  1 token by 4096 x 4096 (8.7 MB) 6.2
-// us: launch and one pass of latency.
+// us: one pass of latency, and a launch that does not overlap the kernel before.
 //
 // Scales multiply the FP32 sums of one group, from which (128 + z) sum x is
 // taken first, with the sums of x from MMAs whose weights are ones; that
@@ -30,7 +32,8 @@
 //
 // FP32 X is split into three BF16 (24 bits) that take three columns of an MMA
 // each token, so a tile holds 2 tokens, and 8 in BF16.  4 tokens by 4096 x
-// 14336 take 31 us, 93 when the split rounded each plane.
+// 14336 take 28.7 us; the step from planes that are rounded to planes that are
+// cut took the same from 93 to 31.
 //
 // A CTA has one block of rows and its warps split k; their sums meet in shared
 // memory in a fixed order.  Where the blocks of rows are few and long, a
@@ -203,7 +206,7 @@ struct Q4Cfg {
   static constexpr int RING = STAGES * SLOT, RED = TI * 16 * COLS * 4;
   static constexpr int WARP_BYTES = RING > RED ? RING : RED;
   // Warps that an SM holds.  With four tiles 8 run faster than 12 (16 x 8192 x
-  // 28672: 68 against 78 us): what shared memory they leave is L1 for x.  With
+  // 28672: 68 against 78 us when they were chosen, 61.5 with 8 now): what shared memory they leave is L1 for x.  With
   // two and two of columns of large groups 12, by their registers (16 x 2048 x
   // 8192: 12.4 us, with 16 warps 16.5), and 8 in FP32 (4 x 4096 x 14336: 28.7
   // us, with 12 32.7).
