@@ -178,21 +178,38 @@ def expert_combine_backward(dO, Y, place, offsets, weights=None, need_dy=True, n
         dO, Y, place, offsets, weights, bool(need_dy), bool(need_dw), _handle(stream))
 
 
+def _items(x):
+    """What x holds, as a list; None for a number (a tensor of no dimension among them)."""
+    try:
+        return list(x)
+    except TypeError:
+        return None
+
+
+def _coefficients(coefficients, steps):
+    """a, b and c, or those of each step one after the other (as many numbers as
+    `steps` takes, which the native module looks at)."""
+    flat = _items(coefficients) or ()
+    rows = [_items(x) for x in flat]
+    if rows and all(r is None for r in rows):
+        return flat
+    if not rows or len(rows) != steps or any(r is None or len(r) != 3 for r in rows):
+        raise ValueError("coefficients must be a, b and c, or those of each step")
+    return [x for r in rows for x in r]
+
+
 def orthogonalize(G, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, out=None, stream=None,
                   workspace=None):
     """The update G (M x N, or a stack of them) with its singular values brought
     to about 1 and its singular vectors kept: X = G / (|G| + eps), then ``steps``
     times X = a X + (b A + c A A) X with A = X X^T (of G^T for M > N).
     ``coefficients``: a, b and c of every step, or a sequence of them, one for
-    each.  The result has G's type and, unless ``out`` says otherwise (which may
-    be G), its order of storage.  Coefficients that let singular values of 1 or
-    less grow beyond 3.8 are refused (see the header)."""
-    flat = list(coefficients)
-    if any(hasattr(c, "__len__") for c in flat):
-        if len(flat) != steps:
-            raise ValueError("coefficients must be a, b and c, or those of each step")
-        flat = [x for c in flat for x in c]
-    return (_module or _native()).orthogonalize(G, steps, flat, eps, out, _handle(stream), workspace)
+    each (or their numbers in a row).  The result has G's type and, unless
+    ``out`` says otherwise (which may be G), its order of storage.  Coefficients
+    that let singular values of 1 or less grow beyond 3.8 are refused (see the
+    header)."""
+    return (_module or _native()).orthogonalize(G, steps, _coefficients(coefficients, steps), eps,
+                                                out, _handle(stream), workspace)
 
 
 def orthogonalize_workspace(M, N, dtype, batch=1) -> int:

@@ -107,3 +107,51 @@ def test_reference(shape):
     one, bound = ref.one_step(G)
     assert float((one - ref.exact(G, 1)).abs().max()) <= 1e-12
     assert bool((bound < 1e-4).all())
+
+
+class _Taken:
+    """A native module that keeps the coefficients it is given."""
+
+    def orthogonalize(self, G, steps, coefficients, *rest):
+        self.got = [float(x) for x in coefficients]
+
+
+@pytest.fixture
+def taken(monkeypatch):
+    module = _Taken()
+    monkeypatch.setattr(ff, "_module", module)
+    return module
+
+
+ROWS = [(1.0, 2.0, 3.0), [4.0, 5.0, 6.0]]
+
+
+@pytest.mark.parametrize("steps, c, want", [
+    (5, (1.0, 2.0, 3.0), [1.0, 2.0, 3.0]), (3, [1, 2, 3], [1.0, 2.0, 3.0]),
+    (3, torch.tensor([1.0, 2.0, 3.0]), [1.0, 2.0, 3.0]),
+    (1, (torch.tensor(1.0), 2.0, 3.0), [1.0, 2.0, 3.0]),
+    (1, [(1.0, 2.0, 3.0)], [1.0, 2.0, 3.0]), (2, ROWS, [1.0, 2.0, 3.0, 4.0, 5.0, 6.0]),
+    (2, ROWS[0] + tuple(ROWS[1]), [1.0, 2.0, 3.0, 4.0, 5.0, 6.0]),
+    (2, iter(ROWS), [1.0, 2.0, 3.0, 4.0, 5.0, 6.0]),
+    (2, torch.tensor(ROWS[1:] + ROWS[:1]), [4.0, 5.0, 6.0, 1.0, 2.0, 3.0]),
+    (3, ROWS + ROWS[:1], [1.0, 2.0, 3.0, 4.0, 5.0, 6.0, 1.0, 2.0, 3.0])], ids=str)
+def test_forms_of_coefficients(taken, steps, c, want):
+    ff.orthogonalize(None, steps=steps, coefficients=c)
+    assert taken.got == want
+
+
+@pytest.mark.parametrize("steps, c", [
+    # rows of other lengths, whose numbers add up to what a call may have
+    (3, [(1.0,), (2.0,), (3.0,)]), (2, [(1.0, 2.0), (3.0, 4.0, 5.0, 6.0)]),
+    (2, [(), (1.0, 2.0, 3.0, 4.0, 5.0, 6.0)]), (2, [(), (1.0, 2.0, 3.0)]),
+    (3, torch.ones(3, 1)), (1, torch.ones(1, 9)),
+    # numbers and rows side by side
+    (2, [1.0, (2.0, 3.0)]), (3, [1.0, (2.0, 3.0), 4.0]), (3, [1.0, 2.0, (3.0,)]),
+    # neither numbers nor rows
+    (1, ()), (0, ()), (1, 1.0), (1, None),
+    (1, torch.tensor(1.0)), (2, [(1.0, 2.0, 3.0)] * 3), (2.5, ROWS), ("all", ROWS),
+    (1, "abc")], ids=str)
+def test_forms_of_coefficients_refused(taken, steps, c):
+    with pytest.raises(ValueError):
+        ff.orthogonalize(None, steps=steps, coefficients=c)
+    assert not hasattr(taken, "got")
