@@ -655,7 +655,8 @@ GEMM_API int expert_combine_backward(int dtype, int w_dtype, int64_t T, int64_t 
  * G and O: row-major, leading dimensions and the matrices' distances in elements
  * (those are not read for one matrix).  A column-major matrix is the
  * row-major storage of its transpose, whose result is the result's transpose.
- * O may be G (the same matrix, not another overlap).
+ * O may be G (the same matrices, not another overlap).  The matrices of G may
+ * share elements, those of O none, but their rows may lie side by side.
  * dtype F32 or BF16, of G and O.  X is kept in FP32 and its term a X is added
  * in FP32.  The factors of the products have 22 bits (F32: errors as of FP32
  * products) or 11 (BF16: they take less from the result than its own rounding

@@ -1008,6 +1008,22 @@ int check_sizes(int dtype, int64_t batch, int64_t M, int64_t N) {
   return GEMM_OK;
 }
 
+// Whether no two of `batch` M x N matrices share an element, whose rows are ldo and
+// which themselves are `stride` elements apart: one after the other, or row by row
+// side by side.
+bool results_apart(int64_t batch, int64_t M, int64_t N, int64_t ldo, int64_t stride) {
+  if (stride < N) return batch < 2 || M == 0 || N == 0;
+  int64_t at = 0;  // where matrix d begins, in the first one's rows
+  for (int64_t d = 1; d < batch; ++d) {
+    if (at > INT64_MAX - stride) return true;
+    at += stride;
+    const int64_t row = at / ldo, col = at % ldo;
+    if (row >= M || (row == M - 1 && col >= N)) return true;  // behind it, as are all others
+    if (col < N || (row + 1 < M && ldo - col < N)) return false;
+  }
+  return true;
+}
+
 template <typename... Params, typename... Args>
 cudaError_t launch_prep(void (*kern)(Params...), dim3 grid, cudaStream_t s, const Args &...args) {
   cudaLaunchAttribute attr[1];
@@ -1086,9 +1102,8 @@ int orthogonalize(int dtype, int64_t batch, int64_t M, int64_t N, const void *G,
   const uintptr_t mask = dtype_size(dtype) - 1;
   const int64_t width = N > 1 ? N : 1;
   if (ldg < width || ldo < width || ldg > kMaxLd || ldo > kMaxLd) return GEMM_ERR_INVALID_ARG;
-  // results of several matrices do not overlap
-  if (batch > 1 && (stride_g < 0 || stride_o < N || (M > 0 && (stride_o - N) / ldo < M - 1)))
-    return GEMM_ERR_INVALID_ARG;
+  if (batch > 1 && (stride_g < 0 || stride_o < 0)) return GEMM_ERR_INVALID_ARG;
+  if (!results_apart(batch, M, N, ldo, stride_o)) return GEMM_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) & 255) return GEMM_ERR_INVALID_ARG;
   if (batch > 0 && M > 0 && N > 0 &&
       (!G || !O || ((reinterpret_cast<uintptr_t>(G) | reinterpret_cast<uintptr_t>(O)) & mask)))

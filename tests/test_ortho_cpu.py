@@ -155,3 +155,30 @@ def test_forms_of_coefficients_refused(taken, steps, c):
     with pytest.raises(ValueError):
         ff.orthogonalize(None, steps=steps, coefficients=c)
     assert not hasattr(taken, "got")
+
+
+def test_matrices_of_the_result_share_nothing(lib):
+    """The call takes the strides of a stack whose matrices have no element in common, rows side by
+    side included, and no others."""
+    if torch.cuda.is_available():
+        pytest.skip("what is taken would run, on addresses that are none")
+    taken = 0
+    for batch in (1, 2, 3, 5):
+        for M in (1, 2, 3):
+            for N in (1, 2, 3):
+                for ldo in range(N, 9):
+                    for so in range(26):
+                        places = [z * so + i * ldo + j for z in range(batch) for i in range(M)
+                                  for j in range(N)]
+                        apart = len(set(places)) == len(places)
+                        taken += apart
+                        want = gemm.ERR_NO_DEVICE if apart else gemm.ERR_INVALID_ARG
+                        got = _call(lib, batch=batch, M=M, N=N, ldg=N, sg=0, ldo=ldo, so=so)
+                        assert got == want, (batch, M, N, ldo, so)
+    assert taken > 1000
+    far = 1 << 62  # three such strides are more than 64 bits hold
+    assert _call(lib, batch=4, so=far) == gemm.ERR_NO_DEVICE
+    assert _call(lib, batch=65535, M=300, N=4, ldg=4, sg=0, ldo=4 * 65535, so=4) == \
+        gemm.ERR_NO_DEVICE
+    assert _call(lib, batch=65535, M=300, N=4, ldg=4, sg=0, ldo=4 * 65535 - 1, so=4) == \
+        gemm.ERR_INVALID_ARG
