@@ -599,13 +599,14 @@ GEMM_API uint64_t grad_norm_clip_workspace(int64_t count);
  * only be aligned to their elements, and outputs overlap no input.
  *
  * expert_sort -- ids: T x k integers of id_bytes (4 or 8) bytes, ldi elements
- * between tokens.  experts: 1 to 1024.
+ * between tokens.  experts: 1 to GEMM_MAX_EXPERTS (GEMM_ERR_UNSUPPORTED beyond).
  * place (T x k, contiguous): the row of each choice, or -1.
  * offsets (experts + 1): the first row of each expert; the last is the number
  * of routed rows.
  * order (T * k, may be NULL): the choice t * k + j of each row, -1 behind the
  * routed ones.
  */
+#define GEMM_MAX_EXPERTS 1024
 GEMM_API int expert_sort(int id_bytes, int64_t T, int64_t k, int64_t experts, const void *ids,
                          int64_t ldi, int32_t *place, int32_t *offsets, int32_t *order,
                          cudaStream_t stream);

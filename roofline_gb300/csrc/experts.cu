@@ -26,7 +26,6 @@ namespace {
 
 // ------------------------------------------------------------------ the sort
 
-constexpr int kMaxExperts = 1024;
 constexpr int kSortWarps = 32;
 constexpr int kSortCluster = 16;
 
@@ -495,7 +494,7 @@ template <typename Id>
 cudaError_t allow_sort(int dev) {
   static Once smem_once, cluster_once;
   auto kern = expert_sort_kernel<Id>;
-  const int most = (kSortWarps + 2) * kMaxExperts * (int)sizeof(int);
+  const int most = (kSortWarps + 2) * GEMM_MAX_EXPERTS * (int)sizeof(int);
   cudaError_t e = allow_shared_memory(smem_once, kern, most, dev);
   const bool known = dev >= 0 && dev < 64;
   if (e != cudaSuccess || (known && cluster_once.done[dev].load(std::memory_order_relaxed)))
@@ -609,7 +608,7 @@ int expert_sort(int id_bytes, int64_t T, int64_t k, int64_t experts, const void 
   int st = check_sizes(T, k, 0, 0);
   if (st != GEMM_OK) return st;
   if (experts < 1 || !offsets || !aligned(offsets, 4)) return GEMM_ERR_INVALID_ARG;
-  if (experts > kMaxExperts) return GEMM_ERR_UNSUPPORTED;
+  if (experts > GEMM_MAX_EXPERTS) return GEMM_ERR_UNSUPPORTED;
   if (!rows_ok(ids, ldi, T, k, id_bytes) || !rows_ok(place, k > 1 ? k : 1, T, k, 4) ||
       (order && !aligned(order, 4)))
     return GEMM_ERR_INVALID_ARG;

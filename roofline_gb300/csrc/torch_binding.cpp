@@ -526,6 +526,9 @@ PyObject *expert_sort_(PyObject *const *a) {
   const int64_t T = e.size(0), k = e.size(1), ld = leading(e, "experts");
   const int64_t count = integer(a[1], "count", 1, INT_MAX);
   const int device = e.get_device();
+  // what the library refuses is refused before memory is taken for it
+  if (count > GEMM_MAX_EXPERTS || (k > 0 && T > INT_MAX / k))
+    throw Failed{GEMM_ERR_UNSUPPORTED, "expert_sort"};
   const OnStream s(a[2], device);
   // one allocation for all three (a microsecond each)
   const int64_t n = T * k;

@@ -281,6 +281,20 @@ def test_refusals(ff):
         ff.expert_sort(torch.zeros((6, 2), dtype=torch.int32, device="cuda"), 1025)
 
 
+def test_too_many_experts_take_no_memory(ff):
+    from roofline_gb300 import gemm
+    ids = torch.zeros((6, 2), dtype=torch.int32, device="cuda")
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for count in (1025, 10 ** 8, 2 ** 31 - 1):
+        with pytest.raises(gemm.GemmError) as refused:
+            ff.expert_sort(ids, count)
+        assert refused.value.code == gemm.ERR_UNSUPPORTED
+    assert torch.cuda.max_memory_allocated() == before
+    ids[1, 1] = 1023
+    assert ff.expert_sort(ids, 1024)[1].tolist() == [0] + 1023 * [11] + [12]
+
+
 def test_on_another_stream_and_in_a_graph(ff):
     X, dO, Y, w, place, offsets, order = _make(ff, 6, 500, 4, 264, BF16)
     g = torch.Generator().manual_seed(8)
