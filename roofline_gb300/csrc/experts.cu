@@ -562,10 +562,14 @@ void shape_rows(RowParams &p, int64_t blocks) {
   const int64_t groups = ceil_div(p.T, kRowThreads / p.lanes);
   while (p.parts * p.lanes < p.vecs && groups * p.parts < blocks) p.parts *= 2;
 }
+// Blocks for the tokens, or as many as there are rows that no choice can have and that
+// zero_rest clears, if those are more (512 MB behind one token's 8 rows, us: gather 2034
+// by the token's own four blocks, 80 with this, gradients 8122 by one and 81).
 int64_t grid_of(const RowParams &p, int sms) {
-  const int64_t items = ceil_div(p.T, kRowThreads / p.lanes) * p.parts;
-  const int64_t most = (int64_t)sms * 16;
-  return items < most ? (items > 0 ? items : 1) : most;
+  int64_t blocks = ceil_div(p.T, kRowThreads / p.lanes) * p.parts;
+  const int64_t behind = p.dy ? p.rows - p.T * p.k : 0, most = (int64_t)sms * 16;
+  if (blocks < behind) blocks = behind;
+  return blocks < most ? (blocks > 0 ? blocks : 1) : most;
 }
 
 // The kernel of a type, vector and number of choices: make(type, bytes of a vector,

@@ -201,6 +201,44 @@ def test_empty_extents(ff):
     assert dY.shape == (10, 0) and bool((dW == 0).all())
 
 
+def _time(f):
+    """Milliseconds of the fastest of some calls."""
+    times = []
+    for _ in range(6):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times[1:])
+
+
+@pytest.mark.parametrize("T", [0, 1, 3])
+def test_long_buffers_of_few_tokens(ff, T):
+    """Rows behind the routed ones are cleared by the whole device, not by the tokens' blocks: half
+    a gigabyte takes about what torch's own zeros take (by one block some 60 times as long)."""
+    k, D, rows = 8, 4096, 65536
+    g = torch.Generator().manual_seed(T)
+    X, w = _mat(g, T, D, BF16), torch.rand((T, k), generator=g).cuda()
+    place, offsets, order = ff.expert_sort(_choices(g, T, k, 16, 0.3).cuda(), 16)
+    n = int(offsets[-1])
+    buf = torch.full((rows, D), 7.0, dtype=BF16, device="cuda")
+    zeros = _time(buf.zero_)
+    buf.fill_(7.0)
+    ff.expert_gather(X, place, offsets, out=buf)
+    assert torch.equal(buf[:n], X[order[:n].long() // k]) and not bool(buf[n:].any())
+    assert _time(lambda: ff.expert_gather(X, place, offsets, out=buf)) < 5 * zeros
+    dY, dw = ff.expert_combine_backward(X, buf, place, offsets, w)
+    (want, bound), dots = ref.combine_backward(X, buf, place, w)
+    at = place.cpu().long()
+    on = at >= 0
+    assert ref.worst(dY[at[on].cuda()], (want[on], bound[on])) <= 1.0 and not bool(dY[n:].any())
+    assert ref.worst(dw, dots) <= 1.0
+    del dY
+    assert _time(lambda: ff.expert_combine_backward(X, buf, place, offsets, w)) < 5 * zeros
+
+
 def test_offsets_beyond_32_bits(ff):
     """Rows of the sorted buffer more than 2^32 bytes and 2^31 elements from its start."""
     T, k, D = 70000, 8, 4096
