@@ -29,6 +29,7 @@
 // added to sums in registers, and the small ones apart (as in ff_tc.cu); BF16's
 // gather over the whole of K, which takes 1.5e-4 off a sum of one sign over
 // 32768 at the most, and beyond that two planes are taken.
+#include <atomic>
 #include <cmath>
 
 #include "ortho.cuh"
@@ -40,6 +41,9 @@ using namespace tc;
 namespace {
 
 __device__ int g_ortho_status;  // 0 = ok, else a GEMM_ERR_* code
+// Whether this process has launched (or captured) the kernels that write it: each word
+// that gemm_check_status reads takes it 10 us.
+std::atomic<bool> g_ortho_ran{false};
 
 // X is kept in FP32 in the order in which the apply step's warps hold it: for
 // 32 rows and 16 columns, the first 8 columns row by row, then the others, so
@@ -1053,6 +1057,7 @@ cudaError_t prepare(const PrepParams &p, int planes, int64_t batch, int blocks, 
 
 int ortho_read_and_clear_status(cudaStream_t s) {
   int v = 0;
+  if (!g_ortho_ran.load(std::memory_order_relaxed)) return ortho_small_read_and_clear_status(s);
   if (cudaMemcpyFromSymbolAsync(&v, g_ortho_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
           cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess) {
@@ -1131,6 +1136,7 @@ int orthogonalize(int dtype, int64_t batch, int64_t M, int64_t N, const void *G,
     st = library_workspace(dev, (size_t)y.end, &given);
     if (st != GEMM_OK) return st;
   }
+  g_ortho_ran.store(true, std::memory_order_relaxed);
   uint8_t *ws = static_cast<uint8_t *>(given);
   auto at = [&](uint64_t offset) { return static_cast<void *>(ws + offset); };
 

@@ -24,7 +24,8 @@ using namespace tc;
 
 namespace {
 
-__device__ int g_small_status;  // 0 = ok, else a GEMM_ERR_* code
+__device__ int g_small_status;           // 0 = ok, else a GEMM_ERR_* code
+std::atomic<bool> g_small_ran{false};    // as g_ortho_ran
 
 constexpr int kThreads = 512;  // 16 warps: four for each 32 rows
 constexpr int kWarps = kThreads / 32, kStep = 16 * kWarps / 4;  // columns of all warps' blocks
@@ -565,6 +566,7 @@ int launch_ortho_small(const OrthoSizes &q, const OrthoCall &call, const DeviceP
                        cudaStream_t s) {
   int64_t waves;
   const Shape shape = shape_of(q, &waves);
+  g_small_ran.store(true, std::memory_order_relaxed);
   SmallParams p{};
   p.g = call.g;
   p.ldg = call.ldg;
@@ -590,6 +592,7 @@ int launch_ortho_small(const OrthoSizes &q, const OrthoCall &call, const DeviceP
 
 int ortho_small_read_and_clear_status(cudaStream_t s) {
   int v = 0;
+  if (!g_small_ran.load(std::memory_order_relaxed)) return GEMM_OK;
   if (cudaMemcpyFromSymbolAsync(&v, g_small_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
           cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess) {
