@@ -13,6 +13,13 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: long-running CPU test")
 
 
+# Tests of the host side that make allowed calls on addresses that are none, which end at
+# "no device" on a machine without a GPU and would be read by kernels on one.
+HOST_ONLY = {"tests/test_experts_cpu.py::" + name
+             for name in ("test_sort_sizes", "test_gather_sizes", "test_combine_sizes",
+                          "test_combine_backward_sizes")}
+
+
 def pytest_collection_modifyitems(config, items):
     try:
         import torch
@@ -20,6 +27,10 @@ def pytest_collection_modifyitems(config, items):
     except Exception:  # pragma: no cover
         have_gpu = False
     if have_gpu:
+        skip = pytest.mark.skip(reason="calls on addresses that are none: for machines without a GPU")
+        for item in items:
+            if "tests/" + item.nodeid.split("tests/")[-1] in HOST_ONLY:
+                item.add_marker(skip)
         return
     skip = pytest.mark.skip(reason="no CUDA GPU in this process")
     for item in items:
