@@ -651,22 +651,30 @@ GEMM_API int expert_combine_backward(int dtype, int w_dtype, int64_t T, int64_t 
  *     A = X X^T,  X = a X + (b A + c A A) X     `steps` times (1 to 64)
  * and O = X; for M > N the same of G^T, O = X^T.  coefficients: HOST array of
  * 3 * steps floats, a, b and c of each step, read before the call returns.
- * With (3.4445, -4.7750, 2.0315) and 5 steps singular values from about 0.01
- * of the norm on end between 0.7 and 1.2.
+ * With (3.4445, -4.7750, 2.0315) and 5 steps singular values from 0.01 of the
+ * norm on end between 0.68 and 1.14.
  * G and O: row-major, leading dimensions and the matrices' distances in elements
  * (those are not read for one matrix).  A column-major matrix is the
  * row-major storage of its transpose, whose result is the result's transpose.
  * O may be G (the same matrices, not another overlap).  The matrices of G may
  * share elements, those of O none, but their rows may lie side by side.
  * dtype F32 or BF16, of G and O.  X is kept in FP32 and its term a X is added
- * in FP32.  The factors of the products have 22 bits (F32: errors as of FP32
- * products) or 11 (BF16: they take less from the result than its own rounding
- * does); sums are in FP32.  They are FP16 values scaled for singular
- * values of up to 3.8 at any step: coefficients that let one of 1 or less grow
- * beyond that, or b A + c A A beyond 60, are refused
- * (GEMM_ERR_UNSUPPORTED), as are sizes with min(M, N) > 2^20 or more than 2^24
- * tiles of 128 x 128.  A norm is exact over the whole range of its type.  An
- * Inf or NaN in a matrix makes all of its result NaN.
+ * in FP32; sums are in FP32.  The factors of the products are scaled FP16
+ * values, of 22 bits for F32: errors as of FP32 products, but for rows of G so
+ * far below the others that the factors' smallest steps, 2^-36, are not small
+ * beside them (rows over 8 orders of magnitude, brought to one size by 64 steps
+ * with (1.5, -0.5, 0): 3e-5 of the result's norm; over 6: 5e-7).  For BF16 they
+ * have 11 bits (22 for a side beyond 32768): 0.3e-3 to 1.9e-3 of the norm after
+ * the 5 steps above, beside 1.7e-3 of the result's own rounding.
+ * The scales set a range for the coefficients.  With s the largest singular value
+ * that a step may find (1, then 1.001 times the most that the steps before make
+ * of those up to 1), every step needs
+ *     s^2 <= 15   |b| + 3 |c| s^2 <= 250   the values of b y + c y^2 for y from 0
+ *     to s^2 all within 60 of each other
+ * and others are refused (GEMM_ERR_UNSUPPORTED), as are min(M, N) > 2^20, a side
+ * beyond 2^31 - 512, more than 65535 matrices or 2^24 tiles of 128 x 128 in all.
+ * A norm is exact over the whole range of its type.  An Inf or NaN in a matrix
+ * makes all of its result NaN.
  * workspace: orthogonalize_workspace() bytes (0 for matrices that stay on chip:
  * one side of up to 128, and not too many), 256-byte aligned, or NULL for the
  * library's per-device buffer (with the rules of gemm_f32_ex).

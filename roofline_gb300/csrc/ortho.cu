@@ -960,7 +960,9 @@ OrthoSizes sizes_of(int dtype, int64_t batch, int64_t M, int64_t N) {
 }
 
 // Whether the singular values, from 1 at most, and what the steps make of them
-// stay where the FP16 factors hold them (t is at most the largest eigenvalue).
+// stay where the FP16 factors hold them: X up to s, U up to l = s s (t is at most the
+// largest eigenvalue), D up to |b| + 2 |c| t + |c| l, and B, which is b x + c x x at an
+// eigenvalue less that at t.
 bool in_range(int steps, const float *abc) {
   double s = 1.0;
   for (int i = 0; i < steps; ++i) {

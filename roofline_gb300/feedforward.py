@@ -43,7 +43,7 @@ ACT_RELU = 3
 ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "relu": ACT_RELU}
 
 # a, b and c of a Newton-Schulz step that brings the singular values from 0.01
-# of the norm to 1 into 0.7 to 1.2 in five
+# of the norm to 1 into 0.68 to 1.14 in five
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
 
 _module = None
@@ -206,8 +206,9 @@ def orthogonalize(G, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, out=None, st
     ``coefficients``: a, b and c of every step, or a sequence of them, one for
     each (or their numbers in a row).  The result has G's type and, unless
     ``out`` says otherwise (which may be G), its order of storage.  Coefficients
-    that let singular values of 1 or less grow beyond 3.8 are refused (see the
-    header)."""
+    are refused (GemmError) where a step could find singular values s beyond 3.8,
+    where |b| + 3 |c| s^2 is beyond 250, and where b A + c A A could span more
+    than 60 (see the header, and there for the accuracy)."""
     return (_module or _native()).orthogonalize(G, steps, _coefficients(coefficients, steps), eps,
                                                 out, _handle(stream), workspace)
 

@@ -182,3 +182,27 @@ def test_matrices_of_the_result_share_nothing(lib):
         gemm.ERR_NO_DEVICE
     assert _call(lib, batch=65535, M=300, N=4, ldg=4, sg=0, ldo=4 * 65535 - 1, so=4) == \
         gemm.ERR_INVALID_ARG
+
+
+# A step's limits one by one: s^2 <= 15, |b| + 3 |c| s^2 <= 250, a span of 60 of b y + c y^2
+@pytest.mark.parametrize("beyond, inside", [
+    ((3.88, 0.0, 0.0, 0.5, 0.0, 0.0), (3.86, 0.0, 0.0, 0.5, 0.0, 0.0)),
+    # singular values of 0.1: b A is 3 at most
+    ((0.1, 0.0, 0.0, 0.0, 300.0, 0.0), (0.1, 0.0, 0.0, 0.0, 249.0, 0.0)),
+    ((0.1, 0.0, 0.0, 0.0, 0.0, 8400.0), (0.1, 0.0, 0.0, 0.0, 0.0, 8200.0)),
+    # |b| + 3 |c| is 61 and 183 at most
+    ((1.0, -61.0, 0.0), (1.0, -59.0, 0.0)), ((1.0, 0.0, 61.0), (1.0, 0.0, 59.0)),
+    # |b| + 3 |c| of 261 and 247, spans of 49 and 44
+    ((1.0, -31.0, 76.5), (1.0, -31.0, 72.0))], ids=str)
+def test_each_limit_of_the_coefficients(lib, beyond, inside):
+    assert _call(lib, steps=len(beyond) // 3, abc=beyond) == gemm.ERR_UNSUPPORTED
+    if not torch.cuda.is_available():
+        assert _call(lib, steps=len(inside) // 3, abc=inside) == gemm.ERR_NO_DEVICE
+
+
+def test_range_of_the_default_coefficients():
+    """Singular values from 0.01 to 1 after five steps."""
+    s = torch.logspace(-2, 0, 200_001, dtype=torch.float64)
+    for a, b, c in ref._steps(ff.NEWTON_SCHULZ, 5):
+        s = ((c * s * s + b) * s * s + a) * s
+    assert 0.68 <= float(s.min()) < 0.69 and 1.13 < float(s.max()) <= 1.14
