@@ -1051,8 +1051,9 @@ cudaError_t prepare(const PrepParams &p, int planes, int64_t batch, int blocks, 
   if (e != cudaSuccess) return e;
   const int64_t most = ceil_div((int64_t)sms * 8, batch);
   const dim3 grid((unsigned)(tiles < most ? tiles : most), (unsigned)batch);
-  return planes == 1 ? launch_prep(ortho_scale_kernel<T, VEC, 1>, grid, s, p, blocks)
-                     : launch_prep(ortho_scale_kernel<T, VEC, 2>, grid, s, p, blocks);
+  if constexpr (std::is_same<T, bf16>::value)  // FP32 always has two planes
+    if (planes == 1) return launch_prep(ortho_scale_kernel<T, VEC, 1>, grid, s, p, blocks);
+  return launch_prep(ortho_scale_kernel<T, VEC, 2>, grid, s, p, blocks);
 }
 
 }  // namespace
