@@ -593,7 +593,8 @@ GEMM_API uint64_t grad_norm_clip_workspace(int64_t count);
  * each expert's rows, and expert_combine adds a token's rows up with its
  * weights.  A choice may be left out (an id outside 0 .. experts - 1, place
  * -1): it has no row, adds nothing and its weight's gradient is 0.  All counts
- * stay on the device, so the calls can be captured into a graph.
+ * stay on the device, so these calls can be captured into a graph; blocks that
+ * run on each expert's rows alone need the offsets on the host.
  * T * k and the rows are less than 2^31, D at most 2^28 (GEMM_ERR_UNSUPPORTED
  * beyond); matrices are row-major with leading dimensions in elements, need
  * only be aligned to their elements, and outputs overlap no input.

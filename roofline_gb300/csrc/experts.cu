@@ -12,10 +12,10 @@
 // The other three move rows and are bound by HBM.  All go token by token: a
 // token's row is read once, whatever the number of its choices, and its
 // choices' rows, the larger part, are written or read in whole lines.  GB300, 8192
-// tokens of 4096 BF16 values: gathered to 8 of 64 experts 98 us (576 MB, 5.9 TB/s), the
-// sort before it 8.5 us (one choice a lane, 16 SMs; 524,288 choices of 256 experts 50 us);
-// 8 rows of each added up 106 us (605 MB, 5.7 TB/s); gradients of 2 rows of each 57 us
-// (336 MB, 5.9 TB/s).  A copy on the same device moves 6.8 TB/s.  Rows that begin
+// tokens of 4096 BF16 values: gathered to 8 of 64 experts 98 us (604 MB, 6.2 TB/s), the
+// sort before it 9 us (one choice a lane, 16 SMs; 524,288 choices of 256 experts 50 us);
+// 8 rows of each added up 107 us (605 MB, 5.7 TB/s); gradients of 2 rows of each 58 us
+// (336 MB, 5.8 TB/s).  A copy on the same device moves 6.8 TB/s.  Rows that begin
 // anywhere are moved in the widest pieces that all of them allow (1025 x 777 FP32, 4
 // bytes: 3 rows of each added up 6.5 us, gradients 7.3 us).
 #include "ff.cuh"

@@ -1,5 +1,5 @@
-// Shared by the feed-forward operators (ff.cu, q4.cu, clip.cu): element types
-// and the activations with their derivatives.
+// Shared by the feed-forward operators (ff.cu, q4.cu, clip.cu, experts.cu, ortho.cu):
+// element types, sums of squares, and the activations with their derivatives.
 #pragma once
 
 #include <cuda_bf16.h>

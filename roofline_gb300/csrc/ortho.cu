@@ -27,8 +27,9 @@
 // Each MMA rounds the sum it adds to towards zero, 2^-24 of it or so.  FP32's
 // large products therefore gather for kFlush K blocks only before they are
 // added to sums in registers, and the small ones apart (as in ff_tc.cu); BF16's
-// gather over the whole of K, which takes 1.5e-4 off a sum of one sign over
-// 32768 at the most, and beyond that two planes are taken.
+// gather over the whole of K, which takes 2e-4 off a sum of one sign over 32768
+// at the most (2048 MMAs, each up to 1.6 * 2^-24: an eighth of the result's own
+// rounding), and beyond that two planes are taken.
 #include <atomic>
 #include <cmath>
 

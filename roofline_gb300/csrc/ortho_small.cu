@@ -1,5 +1,6 @@
-// Orthogonalised updates of matrices whose smaller side m is at most 128, on chip
-// (the steps and their rounding as in ortho.cu).
+// Orthogonalised updates of matrices whose smaller side m is at most 128, on chip.
+// The steps and their planes are those of ortho.cu; D alone is rounded otherwise: it is
+// made of U as its planes hold it, there of the sums before they are rounded to them.
 //
 // The general kernels spend 15 launches of 5 to 8 us on such a matrix, whatever
 // its size.  Here a cluster of up to 16 CTAs holds it for all steps: each CTA has
@@ -470,8 +471,8 @@ struct Shape {
   int cluster, nc;
 };
 // The clusters that take the least time: waves of them, each of 8 and another one for
-// every 4 KB of X's planes of a CTA's 64 rows (us, one wave: BF16 43 with 64 columns, 51
-// with 128, 60 with 256; FP32 61 and 72).
+// every 64 columns of a plane that a CTA has (us, one wave: BF16 40 with 64 columns and 8
+// CTAs, 44 with 16, 47 with 128, 56 with 256; FP32 58 with 64, 63 with 16 CTAs, 69 with 128).
 Shape shape_of(const OrthoSizes &q, int64_t *waves) {
   Shape best{};
   int64_t least = 0;
@@ -552,10 +553,13 @@ int clusters_at_once(int size) {
 }
 
 // Matrices of up to 128 x 4096 (BF16) or 128 x 2048 (FP32), if their clusters run in one
-// wave, or in two from 10 matrices on, by the general kernels / here, us: one of 128 x 512
-// FP32 107 / 62, BF16 86 / 43; 128 x 2000 115 / 72, 91 / 50; 32 of 128 x 512 131 / 70, 103 /
-// 47; two waves, 100 of 128 x 512 BF16 146 / 107, 10 of 128 x 2000 FP32 151 / 143, but 8 of 64
-// x 2048 FP32 109 / 137; three, 40 of 128 x 1024 FP32 200 / 210.
+// wave, or in two from 10 matrices on, by the general kernels / here, us, back to back.  One
+// wave: 32 x 64 FP32 71 / 55, 128 x 512 FP32 105 / 58 and BF16 87 / 40, 128 x 2000 116 / 69 and
+// 94 / 47, 128 x 4000 BF16 100 / 56, 8 of 64 x 1024 FP32 102 / 65, 32 of 128 x 512 134 / 68 and
+// 104 / 46.  Two: 10 of 128 x 2000 FP32 157 / 141, 10 of 128 x 4096 BF16 150 / 111, 20 of 128 x
+// 1000 FP32 156 / 132, 50 of 128 x 512 166 / 131, 100 of 128 x 512 BF16 153 / 104, 300 of 64 x 64
+// FP32 124 / 113; of fewer, 8 of 64 x 2048 FP32 109 / 137.  Three: 40 of 128 x 1024 FP32 200 /
+// 210.
 bool ortho_small_fits(const OrthoSizes &q) {
   if (q.m > kSide || q.n > kMaxCluster * 256 / q.planes) return false;
   int64_t waves = 0;

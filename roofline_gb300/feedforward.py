@@ -16,7 +16,8 @@ that use the outputs, is the caller's part; new outputs are of the given
 stream's memory, so nothing before the call uses them.
 
 No call records a graph for autograd: outputs require no gradient, whatever the
-inputs do.  What is written in place or into ``out`` counts as modified.
+inputs do.  What is written in place or into ``out`` counts as modified; but
+where a call says that it may be an input, ``out`` must not overlap any.
 
 ``workspace``: optional contiguous CUDA tensor used as scratch
 (``gated_ff_workspace``, ``grad_norm_workspace`` or ``orthogonalize_workspace``
