@@ -181,6 +181,8 @@ def expert_combine_backward(dO, Y, place, offsets, weights=None, need_dy=True, n
 
 def _items(x):
     """What x holds, as a list; None for a number (a tensor of no dimension among them)."""
+    if isinstance(x, (int, float)):  # (an exception for each took a call 1 us)
+        return None
     try:
         return list(x)
     except TypeError:
